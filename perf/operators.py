@@ -332,7 +332,7 @@ def _own(s):
     if not c["back"]:
         n, h = gdn.gdn_add_norm(s.x, s.res, s.w, scale=SCALE, w_add=W_ADD, eps=EPS)
         return {"n": n, "h": h}
-    dx, dres, dw = gdn.gdn_add_norm_bwd(s.res, s.w, s.dn, s.dh, dx_dtype=s.x.dtype, scale=SCALE,
+    dx, dres, dw = gdn.gdn_add_norm_bwd(s.res, s.w, s.dn, s.dh, scale=SCALE,
                                         w_add=W_ADD, eps=EPS)
     return {"dx": dx, "dres": dres, "dw": dw}
 
