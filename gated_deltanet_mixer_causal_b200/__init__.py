@@ -18,12 +18,17 @@ import torch
 
 from ._lib import (GDNError, LIB_PATH, gdn_chunk_prefill, gdn_chunk_prefill_noalloc,
                    gdn_chunk_prefill_path, gdn_chunk_prefill_launches, gdn_chunk_prefill_workspace_size, gdn_conv1d_silu, gdn_decode_step,
-                   gdn_decode_tokens, gdn_prefill_noalloc_status, gdn_prefill_status, lib)
+                   gdn_decode_tokens, gdn_prefill_noalloc_status, gdn_prefill_status, lib,
+                   gdn_decode_paged, gdn_pages_copy, gdn_pages_take, gdn_pages_ref, gdn_pages_fork,
+                   gdn_pages_plan, gdn_pages_compact, gdn_gated_norm, gdn_gated_norm_bwd, gdn_add_norm,
+                   gdn_add_norm_bwd, gdn_norm_bwd_workspace_size)
 
 __all__ = ["GDNError", "LIB_PATH", "lib", "gdn_conv1d_silu", "gdn_chunk_prefill",
            "gdn_chunk_prefill_workspace_size", "gdn_chunk_prefill_noalloc", "gdn_chunk_prefill_path", "gdn_chunk_prefill_launches", "gdn_decode_step",
            "gdn_decode_tokens", "gdn_prefill_status", "gdn_prefill_noalloc_status",
-           "prefill_layer", "qkv_views"]
+           "gdn_decode_paged", "gdn_pages_copy", "gdn_pages_take", "gdn_pages_ref", "gdn_pages_fork",
+           "gdn_pages_plan", "gdn_pages_compact", "gdn_gated_norm", "gdn_gated_norm_bwd", "gdn_add_norm",
+           "gdn_add_norm_bwd", "gdn_norm_bwd_workspace_size", "prefill_layer", "qkv_views"]
 
 
 def qkv_views(y: torch.Tensor, Hk: int, Hv: int, d: int):

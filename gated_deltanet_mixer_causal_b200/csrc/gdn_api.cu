@@ -35,6 +35,18 @@ gdn_status_t cuda_status(cudaError_t e, const char* what) {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+// Pages of `bytes` at l * layer + p * page keep apart: either a layer's pages lie behind one
+// another and the layers behind those, or the other way round.
+bool pages_apart(int32_t pages, int64_t page, int32_t layers, int64_t layer, int64_t bytes) {
+  if (page % 16 || layer % 16 || page < 0 || layer < 0) return false;
+  if (pages > 1 && page < bytes) return false;
+  if (layers <= 1 || pages < 1) return true;
+  if (layer < bytes) return false;
+  return layer >= (pages - 1) * page + bytes || page >= (layers - 1) * layer + bytes || pages == 1;
+}
+
 // [a, a + na) and [b, b + nb) share a byte (null or empty ranges never overlap).
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
@@ -364,6 +376,290 @@ gdn_status_t gdn_decode_tokens(const void* x, const void* conv_w, void* conv_sta
                                float scale, gdn_stream_t stream) {
   return gdn_decode_tokens_ex(x, conv_w, conv_state, g, beta, state, GDN_F32, o, dt, B, n_tok, Hk,
                               Hv, dk, dv, scale, stream);
+}
+
+gdn_status_t gdn_decode_paged(const void* x, int64_t x_stride, const void* conv_w, void* conv_pool,
+                              int64_t conv_stride, void* state_pool, int64_t state_stride,
+                              gdn_dtype_t state_dt, int32_t n_pages, const int32_t* read_pages,
+                              const int32_t* write_pages, const int32_t* n_valid, const float* g,
+                              const float* beta, const void* z, int64_t z_stride, const void* norm_w,
+                              float eps, void* o, gdn_dtype_t dt, int32_t B, int32_t n_tok, int32_t Hk,
+                              int32_t Hv, int32_t dk, int32_t dv, float scale, gdn_stream_t stream) {
+  if (!valid_dtype(dt)) return fail(GDN_ERR_UNSUPPORTED, "decode_paged: unknown dtype %d", (int)dt);
+  if (!valid_dtype(state_dt)) return fail(GDN_ERR_UNSUPPORTED, "decode_paged: unknown state dtype %d", (int)state_dt);
+  if (B < 0) return fail(GDN_ERR_INVALID_ARG, "decode_paged: B = %d < 0", B);
+  if (n_tok < 1 || n_tok > 8) return fail(GDN_ERR_INVALID_ARG, "decode_paged: n_tok = %d outside [1, 8]", n_tok);
+  if (Hk <= 0 || Hv <= 0) return fail(GDN_ERR_INVALID_ARG, "decode_paged: Hk, Hv must be > 0");
+  if (Hv % Hk != 0) return fail(GDN_ERR_UNSUPPORTED, "decode_paged: Hv %% Hk != 0 (%d, %d)", Hv, Hk);
+  if (dk != dv || !supported_head_dim(dk))
+    return fail(GDN_ERR_UNSUPPORTED, "decode_paged: head dims dk=%d dv=%d (need dk = dv in {16,32,64,128})", dk, dv);
+  const int64_t G = Hv / Hk, Cc = 2LL * Hk * dk + (int64_t)Hv * dv;
+  if (Cc > 0x7fffffffLL || gdn::decode_paged_smem(n_tok, G, dk) > 224 * 1024)
+    return fail(GDN_ERR_UNSUPPORTED, "decode_paged: %d tokens of %lld value heads per key head exceed shared memory",
+                n_tok, (long long)G);
+  if ((int64_t)B * Hk > 0x7fffffffLL) return fail(GDN_ERR_INVALID_ARG, "decode_paged: B * Hk too large");
+  if (n_pages < 0) return fail(GDN_ERR_INVALID_ARG, "decode_paged: n_pages = %d < 0", n_pages);
+  if (!(eps >= 0)) return fail(GDN_ERR_INVALID_ARG, "decode_paged: eps must be >= 0");
+  const int64_t vals = (int64_t)Hv * dv, page = vals * dk, taps = 3 * Cc;
+  if (x_stride == 0) x_stride = Cc;
+  if (z_stride == 0) z_stride = vals;
+  if (conv_stride == 0) conv_stride = taps;
+  if (state_stride == 0) state_stride = page;
+  if (x_stride < Cc || x_stride % 8 || z_stride < vals || z_stride % 8 || conv_stride < taps || conv_stride % 8 ||
+      state_stride < page || state_stride % 8)
+    return fail(GDN_ERR_INVALID_ARG, "decode_paged: strides (x %lld, z %lld, conv %lld, state %lld) must cover a row "
+                "or page and be multiples of 8", (long long)x_stride, (long long)z_stride, (long long)conv_stride,
+                (long long)state_stride);
+  if (B == 0) return ok();
+  if (!x || !conv_w || !read_pages || !g || !beta || !o || (n_pages > 0 && (!conv_pool || !state_pool)))
+    return fail(GDN_ERR_INVALID_ARG, "decode_paged: x, conv_w, the pools, read_pages, g, beta and o must be non-null");
+  if (!z != !norm_w) return fail(GDN_ERR_INVALID_ARG, "decode_paged: z and norm_w come together");
+  if (!aligned16(x) || !aligned16(conv_w) || !aligned16(conv_pool) || !aligned16(state_pool) || !aligned16(g) ||
+      !aligned16(beta) || !aligned16(z) || !aligned16(norm_w) || !aligned16(o))
+    return fail(GDN_ERR_INVALID_ARG, "decode_paged: pointers must be 16-byte aligned");
+  if (!aligned4(read_pages) || !aligned4(write_pages) || !aligned4(n_valid))
+    return fail(GDN_ERR_INVALID_ARG, "decode_paged: page lists must be 4-byte aligned");
+  const size_t es = elt_size(dt), sts = elt_size(state_dt);
+  const size_t toks = (size_t)B * n_tok, pages = (size_t)n_pages;
+  const size_t cb = pages ? ((pages - 1) * conv_stride + taps) * es : 0;
+  const size_t sb = pages ? ((pages - 1) * state_stride + page) * sts : 0;
+  const size_t ob = toks * vals * es;
+  const void* ro[9] = {x, conv_w, g, beta, z, norm_w, read_pages, write_pages, n_valid};
+  const size_t rob[9] = {((toks - 1) * x_stride + Cc) * es, (size_t)Cc * 4 * es, toks * Hv * 4, toks * Hv * 4,
+                         ((toks - 1) * z_stride + vals) * es, (size_t)dv * es, (size_t)B * 4, toks * 4, (size_t)B * 4};
+  for (int i = 0; i < 9; ++i)
+    if (overlap(ro[i], rob[i], conv_pool, cb) || overlap(ro[i], rob[i], state_pool, sb) || overlap(ro[i], rob[i], o, ob))
+      return fail(GDN_ERR_INVALID_ARG, "decode_paged: an output or a pool overlaps an input");
+  if (overlap(o, ob, conv_pool, cb) || overlap(o, ob, state_pool, sb))
+    return fail(GDN_ERR_INVALID_ARG, "decode_paged: o overlaps a pool");
+  if (overlap(conv_pool, cb, state_pool, sb)) {
+    // interleaved pages: the state's place in a page's record, modulo the common stride
+    const int64_t step = conv_stride * (int64_t)es;
+    int64_t at = (int64_t)((intptr_t)state_pool - (intptr_t)conv_pool) % step;
+    if (at < 0) at += step;
+    if (step != state_stride * (int64_t)sts || at < taps * (int64_t)es || at + page * (int64_t)sts > step)
+      return fail(GDN_ERR_INVALID_ARG, "decode_paged: conv_pool and state_pool overlap");
+  }
+  gdn::PagedDecode a{x, x_stride, conv_w, conv_pool, conv_stride, state_pool, state_stride, n_pages, read_pages,
+                     write_pages, n_valid, g, beta, z, z_stride, norm_w, eps, o, B, n_tok, Hk, Hv, scale};
+  return cuda_status(gdn::launch_decode_paged((int)dt, (int)state_dt, dk, a, (cudaStream_t)stream),
+                     "decode_paged launch");
+}
+
+gdn_status_t gdn_pages_copy(const void* src_pool, int64_t src_page_stride, int64_t src_layer_stride,
+                            int32_t src_pages, void* dst_pool, int64_t dst_page_stride,
+                            int64_t dst_layer_stride, int32_t dst_pages, int64_t page_bytes,
+                            int32_t layers, const int32_t* src, const int32_t* dst, int32_t n,
+                            gdn_stream_t stream) {
+  if (n < 0 || src_pages < 0 || dst_pages < 0 || layers < 0)
+    return fail(GDN_ERR_INVALID_ARG, "pages_copy: negative count");
+  if (page_bytes <= 0 || page_bytes % 16)
+    return fail(GDN_ERR_INVALID_ARG, "pages_copy: page_bytes = %lld must be a positive multiple of 16", (long long)page_bytes);
+  if (src_page_stride == 0) src_page_stride = page_bytes;
+  if (dst_page_stride == 0) dst_page_stride = page_bytes;
+  if (!pages_apart(src_pages, src_page_stride, layers, src_layer_stride, page_bytes) ||
+      !pages_apart(dst_pages, dst_page_stride, layers, dst_layer_stride, page_bytes))
+    return fail(GDN_ERR_INVALID_ARG, "pages_copy: strides must be multiples of 16 bytes that keep the pages apart");
+  if (n > gdn::kPagesMaxList)
+    return fail(GDN_ERR_UNSUPPORTED, "pages_copy: %d entries, at most %d a call", n, gdn::kPagesMaxList);
+  if (n == 0 || layers == 0 || src_pages == 0 || dst_pages == 0) return ok();
+  if (!src_pool || !dst_pool || !src || !dst)
+    return fail(GDN_ERR_INVALID_ARG, "pages_copy: pools and lists must be non-null");
+  if (!aligned16(src_pool) || !aligned16(dst_pool) || !aligned4(src) || !aligned4(dst))
+    return fail(GDN_ERR_INVALID_ARG, "pages_copy: pools must be 16-byte aligned, lists 4-byte aligned");
+  const size_t sb = (size_t)((layers - 1) * src_layer_stride + (src_pages - 1) * src_page_stride + page_bytes);
+  const size_t db = (size_t)((layers - 1) * dst_layer_stride + (dst_pages - 1) * dst_page_stride + page_bytes);
+  if (src_pool == dst_pool) {
+    if (src_pages != dst_pages || src_page_stride != dst_page_stride || (layers > 1 && src_layer_stride != dst_layer_stride))
+      return fail(GDN_ERR_INVALID_ARG, "pages_copy: one pool, but different strides or page counts");
+  } else if (overlap(src_pool, sb, dst_pool, db)) {
+    return fail(GDN_ERR_INVALID_ARG, "pages_copy: the pools overlap");
+  }
+  if (overlap(src, (size_t)n * 4, dst_pool, db) || overlap(dst, (size_t)n * 4, dst_pool, db))
+    return fail(GDN_ERR_INVALID_ARG, "pages_copy: a list overlaps the destination pool");
+  gdn::PagesCopy a{(const char*)src_pool, (char*)dst_pool, page_bytes, src_page_stride, dst_page_stride,
+                   src_layer_stride, dst_layer_stride, src_pages, dst_pages, layers, src, dst, n};
+  return cuda_status(gdn::launch_pages_copy(a, (cudaStream_t)stream), "pages_copy launch");
+}
+
+gdn_status_t gdn_pages_take(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n, int32_t* out,
+                            gdn_stream_t stream) {
+  if (n < 0 || n_pages < 0) return fail(GDN_ERR_INVALID_ARG, "pages_take: negative count");
+  if (n > gdn::kPagesMaxList)
+    return fail(GDN_ERR_UNSUPPORTED, "pages_take: %d entries, at most %d a call", n, gdn::kPagesMaxList);
+  if (n == 0) return ok();
+  if (!out || (n_pages > 0 && !refs)) return fail(GDN_ERR_INVALID_ARG, "pages_take: refs and out must be non-null");
+  if (!aligned4(refs) || !aligned4(src) || !aligned4(out))
+    return fail(GDN_ERR_INVALID_ARG, "pages_take: arrays must be 4-byte aligned");
+  if (overlap(out, (size_t)n * 4, refs, (size_t)n_pages * 4) || overlap(out, (size_t)n * 4, src, (size_t)n * 4) ||
+      overlap(src, (size_t)n * 4, refs, (size_t)n_pages * 4))
+    return fail(GDN_ERR_INVALID_ARG, "pages_take: arrays overlap");
+  return cuda_status(gdn::launch_pages_take(refs, n_pages, src, n, out, (cudaStream_t)stream), "pages_take launch");
+}
+
+gdn_status_t gdn_pages_ref(int32_t* refs, int32_t n_pages, const int32_t* pages, int32_t n, int32_t delta,
+                           gdn_stream_t stream) {
+  if (n < 0 || n_pages < 0) return fail(GDN_ERR_INVALID_ARG, "pages_ref: negative count");
+  if (n == 0 || n_pages == 0) return ok();
+  if (!refs || !pages) return fail(GDN_ERR_INVALID_ARG, "pages_ref: refs and pages must be non-null");
+  if (!aligned4(refs) || !aligned4(pages)) return fail(GDN_ERR_INVALID_ARG, "pages_ref: arrays must be 4-byte aligned");
+  if (overlap(refs, (size_t)n_pages * 4, pages, (size_t)n * 4))
+    return fail(GDN_ERR_INVALID_ARG, "pages_ref: pages overlaps refs");
+  return cuda_status(gdn::launch_pages_ref(refs, n_pages, pages, n, delta, (cudaStream_t)stream), "pages_ref launch");
+}
+
+gdn_status_t gdn_pages_plan(int32_t* refs, int32_t n_pages, int32_t* table, int32_t n_table, int32_t* src,
+                            int32_t* dst, int32_t* map, int32_t* n_live, gdn_stream_t stream) {
+  if (n_table < 0 || n_pages < 0) return fail(GDN_ERR_INVALID_ARG, "pages_plan: negative count");
+  if (!n_live || (n_pages > 0 && (!refs || !map)) || (n_pages > 1 && (!src || !dst)) || (n_table > 0 && !table))
+    return fail(GDN_ERR_INVALID_ARG, "pages_plan: refs, src, dst, map, n_live (and table) must be non-null");
+  const void* arr[6] = {refs, table, src, dst, map, n_live};
+  const size_t half = (size_t)(n_pages / 2) * 4, all = (size_t)n_pages * 4;
+  const size_t by[6] = {all, (size_t)n_table * 4, half, half, all, 4};
+  for (int i = 0; i < 6; ++i) {
+    if (!aligned4(arr[i])) return fail(GDN_ERR_INVALID_ARG, "pages_plan: arrays must be 4-byte aligned");
+    for (int j = 0; j < i; ++j)
+      if (overlap(arr[i], by[i], arr[j], by[j])) return fail(GDN_ERR_INVALID_ARG, "pages_plan: arrays overlap");
+  }
+  return cuda_status(gdn::launch_pages_plan(refs, n_pages, table, n_table, src, dst, map, n_live, (cudaStream_t)stream),
+                     "pages_plan launch");
+}
+
+size_t gdn_norm_bwd_workspace_size(int32_t D) { return D > 0 ? (size_t)D * gdn::kNormParts * sizeof(float) : 0; }
+
+static gdn_status_t gated_norm(const char* who, gdn::GatedNorm a, int64_t T, int32_t dv, gdn_dtype_t dt,
+                               void* workspace, size_t workspace_bytes, gdn_stream_t stream) {
+  if (!valid_dtype(dt)) return fail(GDN_ERR_UNSUPPORTED, "%s: unknown dtype %d", who, (int)dt);
+  if (T < 0) return fail(GDN_ERR_INVALID_ARG, "%s: T = %lld < 0", who, (long long)T);
+  if (a.H <= 0) return fail(GDN_ERR_INVALID_ARG, "%s: Hv must be > 0", who);
+  if (!supported_head_dim(dv)) return fail(GDN_ERR_UNSUPPORTED, "%s: dv = %d (need 16, 32, 64 or 128)", who, dv);
+  if (!(a.eps >= 0)) return fail(GDN_ERR_INVALID_ARG, "%s: eps must be >= 0", who);
+  if (T > 0x7fffffffLL || T * a.H > 0x7fffffffLL)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: %lld tokens of %d heads pass 2^31 - 1 rows; split the call", who, (long long)T, a.H);
+  const int64_t vals = (int64_t)a.H * dv;
+  if (a.z_stride == 0) a.z_stride = vals;
+  if (a.dz_stride == 0) a.dz_stride = vals;
+  if (a.z_stride < vals || a.z_stride % 8 || a.dz_stride < vals || a.dz_stride % 8)
+    return fail(GDN_ERR_INVALID_ARG, "%s: gate strides must cover a token's heads and be multiples of 8", who);
+  if (!aligned16(a.o) || !aligned16(a.z) || !aligned16(a.w) || !aligned16(a.y) || !aligned16(a.dy) ||
+      !aligned16(a.dout) || !aligned16(a.dz) || !aligned16(a.dw) || !aligned16(workspace))
+    return fail(GDN_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", who);
+  const size_t es = elt_size(dt), ob = (size_t)T * vals * es, wb = (size_t)dv * es;
+  const size_t zb = T ? ((size_t)(T - 1) * a.z_stride + vals) * es : 0;
+  const size_t dzb = T ? ((size_t)(T - 1) * a.dz_stride + vals) * es : 0;
+  const size_t need = a.dw ? gdn_norm_bwd_workspace_size(dv) : 0, dwb = a.dw ? (size_t)dv * 4 : 0;
+  a.rows = T * a.H;
+  if (!a.back) {
+    if (T == 0) return ok();
+    if (!a.o || !a.z || !a.w || !a.y) return fail(GDN_ERR_INVALID_ARG, "%s: o, z, w and y must be non-null", who);
+    if ((a.y != a.o && overlap(a.y, ob, a.o, ob)) || overlap(a.y, ob, a.z, zb) || overlap(a.y, ob, a.w, wb))
+      return fail(GDN_ERR_INVALID_ARG, "%s: y overlaps an input", who);
+  } else {
+    if (T > 0 && (!a.o || !a.z || !a.w || !a.dy || !a.dout || !a.dz))
+      return fail(GDN_ERR_INVALID_ARG, "%s: o, z, w, dy, do and dz must be non-null", who);
+    if (workspace_bytes < need || (need > 0 && !workspace))
+      return fail(GDN_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", who, workspace_bytes, need);
+    a.part = (float*)workspace;
+    const void* ro[5] = {a.o, a.z, a.w, a.dy, nullptr};
+    const size_t rob[5] = {ob, zb, wb, ob, 0};
+    const void* out[4] = {a.dout, a.dz, a.dw, workspace};
+    const size_t outb[4] = {ob, dzb, dwb, need};
+    for (int i = 0; i < 4; ++i) {
+      for (int j = 0; j < 4; ++j)
+        if (!(i == 0 && j == 3 && out[i] == ro[j]) && overlap(out[i], outb[i], ro[j], rob[j]))
+          return fail(GDN_ERR_INVALID_ARG, "%s: an output overlaps an input", who);
+      for (int j = 0; j < i; ++j)
+        if (overlap(out[i], outb[i], out[j], outb[j])) return fail(GDN_ERR_INVALID_ARG, "%s: outputs overlap", who);
+    }
+    if (T == 0) {
+      if (!a.dw) return ok();
+      return cuda_status(cudaMemsetAsync(a.dw, 0, dwb, (cudaStream_t)stream), "gated_norm_bwd: clearing dw");
+    }
+  }
+  return cuda_status(gdn::launch_gated_norm((int)dt, dv, a, (cudaStream_t)stream), who);
+}
+
+gdn_status_t gdn_gated_norm(const void* o, const void* z, int64_t z_stride, const void* w, float eps, void* y,
+                            gdn_dtype_t dt, int64_t T, int32_t Hv, int32_t dv, gdn_stream_t stream) {
+  gdn::GatedNorm a{};
+  a.o = o; a.z = z; a.z_stride = z_stride; a.w = w; a.eps = eps; a.y = y; a.H = Hv;
+  return gated_norm("gated_norm", a, T, dv, dt, nullptr, 0, stream);
+}
+
+gdn_status_t gdn_gated_norm_bwd(const void* o, const void* z, int64_t z_stride, const void* w, float eps,
+                                const void* dy, void* dout, void* dz, int64_t dz_stride, float* dw,
+                                gdn_dtype_t dt, int64_t T, int32_t Hv, int32_t dv, void* workspace,
+                                size_t workspace_bytes, gdn_stream_t stream) {
+  gdn::GatedNorm a{};
+  a.o = o; a.z = z; a.z_stride = z_stride; a.w = w; a.eps = eps; a.H = Hv; a.back = true;
+  a.dy = dy; a.dout = dout; a.dz = dz; a.dz_stride = dz_stride; a.dw = dw;
+  return gated_norm("gated_norm_bwd", a, T, dv, dt, workspace, workspace_bytes, stream);
+}
+
+static gdn_status_t add_norm_args(const char* who, const gdn::AddNorm& a, gdn_dtype_t dt, gdn_dtype_t res_dt) {
+  if (!valid_dtype(dt) || !valid_dtype(res_dt))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: unknown dtype %d or %d", who, (int)dt, (int)res_dt);
+  if (a.rows < 0 || a.rows > 0x7fffffffLL) return fail(GDN_ERR_INVALID_ARG, "%s: T = %lld outside [0, 2^31)", who, (long long)a.rows);
+  if (a.D < 1) return fail(GDN_ERR_INVALID_ARG, "%s: D = %d < 1", who, a.D);
+  if (a.D > 16384) return fail(GDN_ERR_UNSUPPORTED, "%s: D = %d > 16384", who, a.D);
+  if (!(a.eps >= 0)) return fail(GDN_ERR_INVALID_ARG, "%s: eps must be >= 0", who);
+  return GDN_OK;
+}
+
+gdn_status_t gdn_add_norm(const void* x, const void* residual, const void* w, float scale, float w_add, float eps,
+                          void* h, gdn_dtype_t res_dt, void* n, gdn_dtype_t dt, int64_t T, int32_t D,
+                          gdn_stream_t stream) {
+  gdn::AddNorm a{};
+  a.x = x; a.w = w; a.scale = scale; a.w_add = w_add; a.eps = eps; a.res = residual; a.h = h; a.n = n;
+  a.rows = T; a.D = D;
+  const gdn_status_t s = add_norm_args("add_norm", a, dt, res_dt);
+  if (s != GDN_OK) return s;
+  if (T == 0) return ok();
+  if (!x || !residual || !w || !h || !n)
+    return fail(GDN_ERR_INVALID_ARG, "add_norm: x, residual, w, h and n must be non-null");
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(w) || !aligned16(h) || !aligned16(n))
+    return fail(GDN_ERR_INVALID_ARG, "add_norm: pointers must be 16-byte aligned");
+  const size_t xb = (size_t)T * D * elt_size(dt), rb = (size_t)T * D * elt_size(res_dt), wb = (size_t)D * elt_size(dt);
+  if ((h != residual && overlap(h, rb, residual, rb)) || overlap(h, rb, x, xb) || overlap(h, rb, w, wb) ||
+      overlap(n, xb, x, xb) || overlap(n, xb, residual, rb) || overlap(n, xb, w, wb) || overlap(n, xb, h, rb))
+    return fail(GDN_ERR_INVALID_ARG, "add_norm: an output overlaps an input or the other output");
+  return cuda_status(gdn::launch_add_norm((int)dt, (int)res_dt, a, (cudaStream_t)stream), "add_norm launch");
+}
+
+gdn_status_t gdn_add_norm_bwd(const void* h, const void* w, const void* dn, const void* dh, float scale, float w_add,
+                              float eps, void* dres, gdn_dtype_t res_dt, void* dx, float* dw, gdn_dtype_t dt,
+                              int64_t T, int32_t D, void* workspace, size_t workspace_bytes, gdn_stream_t stream) {
+  gdn::AddNorm a{};
+  a.w = w; a.scale = scale; a.w_add = w_add; a.eps = eps; a.res = dh; a.h = const_cast<void*>(h);
+  a.n = const_cast<void*>(dn); a.dres = dres; a.dx = dx; a.dw = dw; a.part = (float*)workspace;
+  a.rows = T; a.D = D; a.back = true;
+  const gdn_status_t s = add_norm_args("add_norm_bwd", a, dt, res_dt);
+  if (s != GDN_OK) return s;
+  if (T > 0 && (!h || !w || !dn || !dres))
+    return fail(GDN_ERR_INVALID_ARG, "add_norm_bwd: h, w, dn and dres must be non-null");
+  if (!aligned16(h) || !aligned16(w) || !aligned16(dn) || !aligned16(dh) || !aligned16(dres) || !aligned16(dx) ||
+      !aligned16(dw) || !aligned16(workspace))
+    return fail(GDN_ERR_INVALID_ARG, "add_norm_bwd: pointers must be 16-byte aligned");
+  const size_t need = dw ? gdn_norm_bwd_workspace_size(D) : 0;
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(GDN_ERR_WORKSPACE, "add_norm_bwd: workspace %zu bytes < %zu needed", workspace_bytes, need);
+  const size_t xb = (size_t)T * D * elt_size(dt), rb = (size_t)T * D * elt_size(res_dt);
+  const void* ro[4] = {h, w, dn, dh};
+  const size_t rob[4] = {rb, (size_t)D * elt_size(dt), xb, rb};
+  const void* out[4] = {dres, dx, dw, workspace};
+  const size_t outb[4] = {rb, xb, dw ? (size_t)D * 4 : 0, need};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (!(i == 0 && j == 3 && out[i] == ro[j]) && overlap(out[i], outb[i], ro[j], rob[j]))
+        return fail(GDN_ERR_INVALID_ARG, "add_norm_bwd: an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], outb[i], out[j], outb[j])) return fail(GDN_ERR_INVALID_ARG, "add_norm_bwd: outputs overlap");
+  }
+  if (T == 0) {
+    if (!dw) return ok();
+    return cuda_status(cudaMemsetAsync(dw, 0, (size_t)D * 4, (cudaStream_t)stream), "add_norm_bwd: clearing dw");
+  }
+  return cuda_status(gdn::launch_add_norm((int)dt, (int)res_dt, a, (cudaStream_t)stream), "add_norm_bwd launch");
 }
 
 }  // extern "C"

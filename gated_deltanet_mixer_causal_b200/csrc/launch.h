@@ -65,6 +65,61 @@ cudaError_t launch_prefill_chunk_tc(const void* q, const void* k, const void* v,
                                     float scale, BlockStates blocks, void* workspace,
                                     cudaStream_t stream);
 
+// The paged decode's arguments (validated): pools with page strides in elements.
+struct PagedDecode {
+  const void* x; int64_t x_stride;          // [B, n_tok, Cc], a token every x_stride elements
+  const void* conv_w;
+  void* conv_pool; int64_t conv_stride;
+  void* state_pool; int64_t state_stride;
+  int32_t n_pages;
+  const int32_t* read_pages;                // [B]
+  const int32_t* write_pages;               // [B, n_tok] or null: the last state to the page read
+  const int32_t* n_valid;                   // [B] or null: n_tok
+  const float* g; const float* beta;        // [B, n_tok, Hv]
+  const void* z; int64_t z_stride;          // output gate [B, n_tok, Hv, dv] or null
+  const void* norm_w; float eps;
+  void* o;                                  // [B, n_tok, Hv, dv]
+  int32_t B, n_tok, Hk, Hv;
+  float scale;
+};
+size_t decode_paged_smem(int n_tok, int64_t G, int d);
+cudaError_t launch_decode_paged(int dtype, int state_dtype, int d, const PagedDecode& a, cudaStream_t stream);
+
+// Page copies: strides in bytes; every page a multiple of 16 bytes.
+constexpr int kPagesMaxList = 2048;
+struct PagesCopy {
+  const char* src_pool; char* dst_pool;
+  int64_t page_bytes, src_page, dst_page, src_layer, dst_layer;
+  int32_t src_pages, dst_pages, layers;
+  const int32_t* src; const int32_t* dst; int32_t n;
+};
+cudaError_t launch_pages_copy(const PagesCopy& a, cudaStream_t stream);
+cudaError_t launch_pages_take(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n, int32_t* out,
+                              cudaStream_t stream);
+cudaError_t launch_pages_ref(int32_t* refs, int32_t n_pages, const int32_t* pages, int32_t n, int32_t delta,
+                             cudaStream_t stream);
+cudaError_t launch_pages_plan(int32_t* refs, int32_t n_pages, int32_t* table, int32_t n_table, int32_t* src,
+                              int32_t* dst, int32_t* map, int32_t* n_live, cudaStream_t stream);
+
+// Norms. Weight gradients go through at most kNormParts rows of fp32 parts in `part`.
+constexpr int kNormParts = 592;
+struct GatedNorm {
+  const void *o, *z; int64_t z_stride; const void* w; float eps;
+  void* y;                                  // forward
+  const void* dy; void *dout, *dz; int64_t dz_stride; float *dw, *part;   // backward
+  int64_t rows; int32_t H; bool back;
+};
+struct AddNorm {
+  const void *x, *w; float scale, w_add, eps;
+  const void* res;                          // forward: the residual; backward: dh or null
+  void* h;                                  // forward: written; backward: read
+  void* n;                                  // forward: written; backward: dn, read
+  void *dres, *dx; float *dw, *part;        // backward
+  int64_t rows; int32_t D; bool back;
+};
+cudaError_t launch_gated_norm(int dtype, int d, const GatedNorm& a, cudaStream_t stream);
+cudaError_t launch_add_norm(int dtype, int res_dtype, const AddNorm& a, cudaStream_t stream);
+
 // Workspace bytes the prefill path chosen for these arguments needs (0 for the
 // token-recurrent path, which takes no workspace); SIZE_MAX for unsupported shapes.
 size_t prefill_workspace_need(gdn_dtype_t dt, int64_t T, int32_t n_seq, int32_t Hk, int32_t Hv,

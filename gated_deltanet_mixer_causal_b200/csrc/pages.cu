@@ -1,0 +1,273 @@
+// pages.cu -- the pages of a state pool: copy, take, reference counts, compaction plan.
+//
+// A page holds one sequence's state (or its conv taps) of one layer. A copy moves whole pages,
+// so it is bound by HBM: 2 x page bytes for each entry. The lists, counts and plans are a few
+// ints per page and run in one CTA.
+#include "common.cuh"
+#include "launch.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kCopyThreads = 512;
+constexpr int kPlanThreads = 1024;
+
+// Exclusive prefix sum of v over a CTA of WARPS warps, and the total.
+template <int WARPS> __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, m);
+    if (lane >= m) x += y;
+  }
+  __syncthreads();                    // the previous call's sums have been read
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int s = lane < WARPS ? warp_sums[lane] : 0;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, m);
+      if (lane >= m) s += y;
+    }
+    if (lane < WARPS) warp_sums[lane] = s;
+  }
+  __syncthreads();
+  total = warp_sums[WARPS - 1];
+  return (warp ? warp_sums[warp - 1] : 0) + x - v;
+}
+
+// ------------------------------------------------------------------------------- copy
+//
+// Entry i moves page src[i] to page dst[i], as if every source were read before any destination
+// is written. Each CTA works the list out for itself: a hash table of the destinations in
+// shared memory gives the last entry of each (the one that counts). A tile is a run of columns
+// of some entries; the tile's loads go to registers, a barrier, then its stores. Where a source
+// is also a destination, a tile takes its columns of ALL entries, so no other CTA touches them
+// and the barrier is the only order needed; else a tile takes one entry's columns.
+
+struct Table {
+  int32_t* key;    // destination page, -1: empty
+  int32_t* val;    // its last entry
+  uint32_t mask;
+};
+
+__device__ __forceinline__ uint32_t slot_of(int32_t page, uint32_t mask) { return ((uint32_t)page * 2654435761u >> 7) & mask; }
+
+__device__ __forceinline__ int find(const Table& t, int32_t page) {
+  uint32_t s = slot_of(page, t.mask);
+  while (true) {                      // the table is at most half full, so an empty slot ends it
+    const int32_t k = t.key[s];
+    if (k == page) return t.val[s];
+    if (k == -1) return -1;
+    s = (s + 1) & t.mask;
+  }
+}
+
+template <int U>
+__global__ void __launch_bounds__(kCopyThreads, 2)
+pages_copy_kernel(const PagesCopy a, uint32_t slots) {
+  extern __shared__ int32_t sm[];
+  Table tab{sm, sm + slots, slots - 1};
+  int32_t* ms = sm + 2 * slots;       // [n] sources of the entries that count
+  int32_t* md = ms + a.n;             // [n] their destinations
+  __shared__ int clash, sums[32];
+  if (threadIdx.x == 0) clash = 0;
+  for (uint32_t s = threadIdx.x; s < slots; s += kCopyThreads) { tab.key[s] = -1; tab.val[s] = -1; }
+  __syncthreads();
+  auto counts = [&](int i, int32_t& s, int32_t& d) {
+    s = a.src[i]; d = a.dst[i];
+    return s >= 0 && s < a.src_pages && d >= 0 && d < a.dst_pages;
+  };
+  for (int i = threadIdx.x; i < a.n; i += kCopyThreads) {
+    int32_t s, d;
+    if (!counts(i, s, d)) continue;
+    uint32_t h = slot_of(d, tab.mask);
+    while (true) {
+      const int32_t was = atomicCAS(&tab.key[h], -1, d);
+      if (was == -1 || was == d) break;
+      h = (h + 1) & tab.mask;
+    }
+    atomicMax(&tab.val[h], i);
+  }
+  __syncthreads();
+  const bool same = a.src_pool == a.dst_pool;
+  // the entries that count, in the list's order: every CTA must number them alike
+  int m = 0;
+  for (int i0 = 0; i0 < a.n; i0 += kCopyThreads) {
+    const int i = i0 + threadIdx.x;
+    int32_t s = -1, d = -1;
+    const bool on = i < a.n && counts(i, s, d) && find(tab, d) == i && !(same && s == d);
+    int total;
+    const int at = m + block_scan<kCopyThreads / 32>(on, sums, total);
+    if (on) {
+      ms[at] = s; md[at] = d;
+      if (same && find(tab, s) >= 0) clash = 1;
+    }
+    m += total;
+  }
+  __syncthreads();
+  if (m == 0) return;
+
+  // the tile: mm entries x w bytes, mm w = the CTA's registers
+  constexpr int64_t kTile = (int64_t)kCopyThreads * U * 16;
+  int64_t w = 16;
+  if (clash) {
+    while (w * 2 * m <= kTile) w *= 2;
+  } else {
+    while (w < a.page_bytes && w < kTile) w *= 2;
+  }
+  const int mm = (int)(kTile / w), units = (int)(w / 16);
+  const int64_t cols = (a.page_bytes + w - 1) / w, groups = (m + mm - 1) / mm;
+  const int64_t tiles = cols * groups * a.layers;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t grp = tile % groups, rest = tile / groups;
+    const int64_t col = (rest % cols) * w, layer = rest / cols;
+    uint4 v[U];
+    char* to[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int idx = u * kCopyThreads + threadIdx.x;
+      const int64_t e = grp * mm + idx / units, off = col + (int64_t)(idx % units) * 16;
+      to[u] = nullptr;
+      if (e < m && off < a.page_bytes) {
+        to[u] = a.dst_pool + layer * a.dst_layer + (int64_t)md[e] * a.dst_page + off;
+        v[u] = *reinterpret_cast<const uint4*>(a.src_pool + layer * a.src_layer + (int64_t)ms[e] * a.src_page + off);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (to[u]) *reinterpret_cast<uint4*>(to[u]) = v[u];
+  }
+}
+
+// ------------------------------------------------------------------- lists and counts
+
+// out[i] = the next lowest free page for every entry that wants one, -1 for the others
+__global__ void __launch_bounds__(kPlanThreads)
+pages_take_kernel(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n, int32_t* out) {
+  __shared__ int sums[32];
+  __shared__ int32_t want[kPagesMaxList];
+  int n_want = 0, total;
+  for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+    const int i = i0 + threadIdx.x;
+    const bool w = i < n && (!src || (src[i] >= 0 && src[i] < n_pages));
+    const int at = n_want + block_scan<kPlanThreads / 32>(w, sums, total);
+    if (w) want[at] = i;
+    if (i < n) out[i] = -1;
+    n_want += total;
+  }
+  __syncthreads();
+  int taken = 0;
+  for (int64_t p0 = 0; p0 < n_pages && taken < n_want; p0 += kPlanThreads) {
+    const int64_t p = p0 + threadIdx.x;
+    const bool is_free = p < n_pages && refs[p] <= 0;
+    const int at = taken + block_scan<kPlanThreads / 32>(is_free, sums, total);
+    if (is_free && at < n_want) { out[want[at]] = (int32_t)p; refs[p] = 1; }
+    taken += total;
+  }
+}
+
+// refs[p] += delta for each entry, never below 0
+__global__ void __launch_bounds__(kPlanThreads)
+pages_ref_kernel(int32_t* refs, int32_t n_pages, const int32_t* pages, int32_t n, int32_t delta) {
+  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+    const int32_t p = pages[i];
+    if (p >= 0 && p < n_pages) atomicAdd(&refs[p], delta);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+    const int32_t p = pages[i];
+    if (p >= 0 && p < n_pages) atomicMax(&refs[p], 0);
+  }
+}
+
+// The i-th hole below the number of live pages takes the i-th live page behind it.
+__global__ void __launch_bounds__(kPlanThreads)
+pages_plan_kernel(int32_t* refs, int32_t n_pages, int32_t* table, int32_t n_table, int32_t* src,
+                  int32_t* dst, int32_t* map, int32_t* n_live) {
+  __shared__ int sums[32];
+  int total, live_all = 0;
+  for (int64_t p0 = 0; p0 < n_pages; p0 += kPlanThreads) {
+    const int64_t p = p0 + threadIdx.x;
+    const bool live = p < n_pages && refs[p] > 0;
+    block_scan<kPlanThreads / 32>(live, sums, total);
+    live_all += total;
+    if (p < n_pages) map[p] = live ? (int32_t)p : -1;
+  }
+  const int half = n_pages / 2;
+  for (int i = threadIdx.x; i < half; i += kPlanThreads) src[i] = dst[i] = -1;
+  __syncthreads();
+  int holes = 0, movers = 0;
+  for (int64_t p0 = 0; p0 < n_pages; p0 += kPlanThreads) {
+    const int64_t p = p0 + threadIdx.x;
+    const bool in = p < n_pages, live = in && refs[p] > 0;
+    const bool hole = in && !live && p < live_all, mover = live && p >= live_all;
+    const int hat = holes + block_scan<kPlanThreads / 32>(hole, sums, total);
+    holes += total;
+    const int mat = movers + block_scan<kPlanThreads / 32>(mover, sums, total);
+    movers += total;
+    if (hole) dst[hat] = (int32_t)p;
+    if (mover) src[mat] = (int32_t)p;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < movers; i += kPlanThreads) {
+    const int32_t s = src[i], d = dst[i];
+    refs[d] = refs[s];
+    refs[s] = 0;
+    map[s] = d;
+  }
+  // a free page's count is 0, also where a caller left it below
+  __syncthreads();
+  for (int64_t p = live_all + threadIdx.x; p < n_pages; p += kPlanThreads) refs[p] = 0;
+  for (int i = threadIdx.x; i < n_table; i += kPlanThreads) {
+    const int32_t p = table[i];
+    if (p >= 0 && p < n_pages) table[i] = map[p];
+  }
+  if (threadIdx.x == 0) *n_live = live_all;
+}
+
+template <int U>
+cudaError_t launch_copy(const PagesCopy& a, int sms, cudaStream_t st) {
+  uint32_t slots = 32;
+  while (slots < 2u * (uint32_t)a.n) slots *= 2;
+  const size_t smem = sizeof(int32_t) * (2 * (size_t)slots + 2 * (size_t)a.n);
+  if (smem > 40 * 1024) {   // beside the kernel's few static bytes
+    cudaError_t e = cudaFuncSetAttribute(pages_copy_kernel<U>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  pages_copy_kernel<U><<<sms * 2, kCopyThreads, smem, st>>>(a, slots);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_pages_copy(const PagesCopy& a, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  return launch_copy<4>(a, sms, st);
+}
+
+cudaError_t launch_pages_take(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n, int32_t* out,
+                              cudaStream_t st) {
+  pages_take_kernel<<<1, kPlanThreads, 0, st>>>(refs, n_pages, src, n, out);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_ref(int32_t* refs, int32_t n_pages, const int32_t* pages, int32_t n, int32_t delta,
+                             cudaStream_t st) {
+  pages_ref_kernel<<<1, kPlanThreads, 0, st>>>(refs, n_pages, pages, n, delta);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_plan(int32_t* refs, int32_t n_pages, int32_t* table, int32_t n_table, int32_t* src,
+                              int32_t* dst, int32_t* map, int32_t* n_live, cudaStream_t st) {
+  pages_plan_kernel<<<1, kPlanThreads, 0, st>>>(refs, n_pages, table, n_table, src, dst, map, n_live);
+  return cudaGetLastError();
+}
+
+}  // namespace gdn

@@ -335,6 +335,163 @@ gdn_status_t gdn_decode_tokens_ex(const void* x, const void* conv_w, void* conv_
                                   int32_t n_tok, int32_t Hk, int32_t Hv, int32_t dk, int32_t dv,
                                   float scale, gdn_stream_t stream);
 
+/*
+ * gdn_decode_paged -- up to n_tok tokens for each of B sequences whose conv taps and states lie
+ * in the pages of two pools: the decode step of a server that keeps, forks and frees the states
+ * of many requests.
+ *
+ * Per sequence b, for t = 0 .. n_valid[b] - 1, gdn_decode_tokens' update (the conv with the
+ * carried taps, SiLU, the L2 norms, the gated delta rule) starting from page read_pages[b]; the
+ * taps and the state after token t go to page write_pages[b, t]. So a plain decode step writes
+ * the page it reads; a fork reads a shared page and writes its own; a speculative verify step
+ * gives every drafted token a page and later keeps the one of the last accepted token, or
+ * stores nothing and is called again with n_valid = the accepted tokens.
+ *
+ * x            token t of sequence b at x + (b*n_tok + t)*x_stride (elements), dtype dt, Cc
+ *              channels of pre-conv q|k|v. x_stride = 0 means Cc; else >= Cc, a multiple of 8
+ *              (x may be the front of a wider projection).
+ * conv_w       [Cc, 4] dtype dt.
+ * conv_pool    n_pages pages of [3, Cc] dtype dt, oldest tap first, page p at conv_pool +
+ *              p*conv_stride (elements; 0 means dense, else a multiple of 8).
+ * state_pool   n_pages pages of [Hv, dv, dk] of state_dt (GDN_F32, or GDN_BF16: widened to fp32
+ *              on load, rounded once, to nearest even, by each store; between the tokens of a
+ *              call the state stays fp32), page p at state_pool + p*state_stride likewise. The
+ *              pages of the two pools may be interleaved in one buffer (equal strides in bytes).
+ * read_pages   device int32 [B]. A value outside [0, n_pages) (-1 by convention) is a sequence
+ *              that begins here: zero taps, zero state.
+ * write_pages  device int32 [B, n_tok], or NULL: the state after the last valid token goes back
+ *              to read_pages[b]. A value outside [0, n_pages) stores nothing. Where two tokens of
+ *              one sequence name the same page, the later one's state is kept.
+ * n_valid      device int32 [B], clamped to [0, n_tok], or NULL (every token). Nothing is read,
+ *              written or stored for the tokens behind it, and nothing at all for a sequence of
+ *              none: its rows of o stay as they were.
+ * g, beta      [B, n_tok, Hv] fp32.
+ * z, norm_w    both NULL, or the gate [B, n_tok, Hv, dv] (a token every z_stride elements, 0:
+ *              dense) and the weight [dv], dtype dt: o is then gdn_gated_norm's result with eps.
+ * o            [B, n_tok, Hv, dv] dtype dt.
+ * A page that one sequence writes must not be read or written by another one in the same call
+ * (their order is not defined); any number of sequences may read one page that none writes.
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG (n_tok outside [1, 8], bad strides, pointers or overlap),
+ * GDN_ERR_UNSUPPORTED (as gdn_decode_tokens), GDN_ERR_CUDA. B = 0 is a no-op. One launch, no
+ * workspace.
+ */
+gdn_status_t gdn_decode_paged(const void* x, int64_t x_stride, const void* conv_w, void* conv_pool,
+                              int64_t conv_stride, void* state_pool, int64_t state_stride,
+                              gdn_dtype_t state_dt, int32_t n_pages, const int32_t* read_pages,
+                              const int32_t* write_pages, const int32_t* n_valid, const float* g,
+                              const float* beta, const void* z, int64_t z_stride, const void* norm_w,
+                              float eps, void* o, gdn_dtype_t dt, int32_t B, int32_t n_tok, int32_t Hk,
+                              int32_t Hv, int32_t dk, int32_t dv, float scale, gdn_stream_t stream);
+
+/*
+ * gdn_pages_copy -- page src[i] of one pool to page dst[i] of another, or of the same pool, for
+ * each of n entries and in every layer.
+ *
+ * The result is as if every source were read before any destination is written, so one call may
+ * permute the pages of a pool (the reordering of beams) or fill many from one (a fork). Where
+ * several entries name one destination the last of them counts. An entry whose source or
+ * destination is not a page of its pool is skipped.
+ *
+ * src_pool, dst_pool  page p of layer l at pool + l*layer_stride + p*page_stride (bytes, all
+ *              multiples of 16; page_stride 0 means page_bytes). Pages hold any type. They must
+ *              not overlap one another; the pools are either the same one (equal pointers,
+ *              strides and page counts) or do not overlap.
+ * page_bytes   a positive multiple of 16.
+ * src, dst     device int32 [n], n <= 2048.
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED (n > 2048: split the list where the
+ * parts do not depend on one another's order), GDN_ERR_CUDA. n = 0 is a no-op. One launch, no
+ * workspace.
+ */
+gdn_status_t gdn_pages_copy(const void* src_pool, int64_t src_page_stride, int64_t src_layer_stride,
+                            int32_t src_pages, void* dst_pool, int64_t dst_page_stride,
+                            int64_t dst_layer_stride, int32_t dst_pages, int64_t page_bytes,
+                            int32_t layers, const int32_t* src, const int32_t* dst, int32_t n,
+                            gdn_stream_t stream);
+
+/*
+ * gdn_pages_take, gdn_pages_ref, gdn_pages_plan -- the counts of a pool's pages: refs, device
+ * int32 [n_pages], how many holders each page has; 0 (or less) is a free page.
+ *
+ * gdn_pages_take: out[i] (device int32 [n], n <= 2048) receives the lowest free page not taken
+ *   before it, whose count becomes 1, for i = 0, 1, ...; -1 once none is free. With src (device
+ *   int32 [n]) an entry whose src[i] is not a page gets -1 and takes none: gdn_pages_copy(src,
+ *   out) then completes a fork.
+ * gdn_pages_ref: refs[pages[i]] += delta for every entry that is a page (a page listed twice
+ *   counts twice); counts below 0 become 0. delta = 1 shares pages, -1 frees them.
+ * gdn_pages_plan: the moves that bring the live pages to the front: with n_live of them, the
+ *   i-th free page below n_live takes the i-th live page at or behind it. src, dst (device int32
+ *   [n_pages / 2]) receive the moves, padded with -1, for gdn_pages_copy; refs moves with the
+ *   pages; map (device int32 [n_pages]) receives each live page's new place and -1 for free
+ *   ones; table (device int32 [n_table], may be NULL with n_table = 0) is rewritten through map
+ *   (entries that are not pages stay); n_live (device int32 [1]). Sources and destinations are
+ *   distinct, so a long list may be copied in parts.
+ * Each is one launch of one CTA. Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED
+ * (n > 2048 in gdn_pages_take), GDN_ERR_CUDA. n = 0 is a no-op.
+ */
+gdn_status_t gdn_pages_take(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n,
+                            int32_t* out, gdn_stream_t stream);
+gdn_status_t gdn_pages_ref(int32_t* refs, int32_t n_pages, const int32_t* pages, int32_t n,
+                           int32_t delta, gdn_stream_t stream);
+gdn_status_t gdn_pages_plan(int32_t* refs, int32_t n_pages, int32_t* table, int32_t n_table,
+                            int32_t* src, int32_t* dst, int32_t* map, int32_t* n_live,
+                            gdn_stream_t stream);
+
+/*
+ * gdn_gated_norm -- the norm and gate of the mixer's output, per token and value head:
+ *
+ *   y = o / sqrt(mean(o^2) + eps) * w * SiLU(z)          mean over the head's dv values
+ *
+ * o, y         [T, Hv, dv] dtype dt. y may equal o.
+ * z            token t, head h at z + t*z_stride + h*dv (elements), dtype dt; 0 means Hv*dv, else
+ *              >= Hv*dv, a multiple of 8.
+ * w            [dv] dtype dt.
+ * Math in fp32, one rounding to dt. dv in {16, 32, 64, 128}; T*Hv < 2^31. eps >= 0.
+ *
+ * gdn_gated_norm_bwd -- its backward pass: from dy, the gradients
+ *   do [T, Hv, dv], dz (strided by dz_stride like z), dtype dt, and
+ *   dw [dv] fp32 (summed in fp32 in a fixed order: the same inputs give the same bits), or NULL.
+ * dout may equal dy; no other output may overlap an input. workspace:
+ * gdn_norm_bwd_workspace_size(dv) bytes, 16-byte aligned (NULL when dw is NULL); contents on
+ * entry are ignored; not to be used by overlapping calls.
+ * T = 0 is valid (dw is then set to zero). Returns GDN_OK, GDN_ERR_INVALID_ARG,
+ * GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_ERR_CUDA.
+ */
+gdn_status_t gdn_gated_norm(const void* o, const void* z, int64_t z_stride, const void* w, float eps,
+                            void* y, gdn_dtype_t dt, int64_t T, int32_t Hv, int32_t dv,
+                            gdn_stream_t stream);
+gdn_status_t gdn_gated_norm_bwd(const void* o, const void* z, int64_t z_stride, const void* w, float eps,
+                                const void* dy, void* dout, void* dz, int64_t dz_stride, float* dw,
+                                gdn_dtype_t dt, int64_t T, int32_t Hv, int32_t dv, void* workspace,
+                                size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * gdn_add_norm -- the residual add and the norm before a block, per token:
+ *
+ *   h = residual + scale * x;   n = h / sqrt(mean(h^2) + eps) * (w + w_add)
+ *
+ * x, n         [T, D] dtype dt.      residual, h  [T, D] dtype res_dt; h may equal residual.
+ * w            [D] dtype dt; w_add is 0, or 1 for weights kept as their distance from one.
+ * Math in fp32: n comes from the sum before it is rounded to res_dt. 1 <= D <= 16384.
+ *
+ * gdn_add_norm_bwd -- its backward pass, at the h that the forward pass stored: from dn (dtype
+ * dt) and dh (dtype res_dt, the gradient that reaches h on its own way, or NULL for zero),
+ *   dres [T, D] res_dt = the whole gradient of h, which is the residual's; may equal dh,
+ *   dx   [T, D] dt     = scale * that gradient, or NULL,
+ *   dw   [D] fp32 (fixed order, as above), or NULL.
+ * workspace: gdn_norm_bwd_workspace_size(D) bytes, as above.
+ * T = 0 is valid (dw is then set to zero). Return codes as above.
+ */
+gdn_status_t gdn_add_norm(const void* x, const void* residual, const void* w, float scale, float w_add,
+                          float eps, void* h, gdn_dtype_t res_dt, void* n, gdn_dtype_t dt, int64_t T,
+                          int32_t D, gdn_stream_t stream);
+gdn_status_t gdn_add_norm_bwd(const void* h, const void* w, const void* dn, const void* dh, float scale,
+                              float w_add, float eps, void* dres, gdn_dtype_t res_dt, void* dx, float* dw,
+                              gdn_dtype_t dt, int64_t T, int32_t D, void* workspace,
+                              size_t workspace_bytes, gdn_stream_t stream);
+
+/* Bytes of workspace the norms' backward passes need for rows of D values. */
+size_t gdn_norm_bwd_workspace_size(int32_t D);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif
