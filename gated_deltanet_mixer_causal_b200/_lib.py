@@ -52,8 +52,7 @@ SIGNATURES = {
     "gdn_decode_paged": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _P, _I64, ctypes.c_int, _I32, _P, _P,
                                         _P, _P, _P, _P, _I64, _P, _F32, _P, ctypes.c_int, _I32, _I32,
                                         _I32, _I32, _I32, _I32, _F32, _P]),
-    "gdn_pages_copy": (ctypes.c_int, [_P, _I64, _I64, _I32, _P, _I64, _I64, _I32, _I64, _I32, _P, _P,
-                                      _I32, _P]),
+    "gdn_pages_copy": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _P, _I32, _P]),
     "gdn_pages_take": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P]),
     "gdn_pages_ref": (ctypes.c_int, [_P, _I32, _P, _I32, _I32, _P]),
     "gdn_pages_plan": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _P, _P, _P]),
@@ -66,6 +65,14 @@ SIGNATURES = {
                                         ctypes.c_int, _I64, _I32, _P, _SZ, _P]),
     "gdn_norm_bwd_workspace_size": (_SZ, [_I32]),
 }
+
+
+
+class _PagePool(ctypes.Structure):      # gdn_page_pool_t
+    _fields_ = [("src", _P), ("dst", _P), ("page_bytes", _I64), ("src_page_stride", _I64),
+                ("src_layer_stride", _I64), ("dst_page_stride", _I64), ("dst_layer_stride", _I64),
+                ("layers", _I32)]
+
 
 _lib = None
 
@@ -360,47 +367,73 @@ def gdn_decode_tokens(x: torch.Tensor, conv_w: torch.Tensor, conv_state: torch.T
 
 
 # ------------------------------------------------------- paged decode, pages, norms around a block
+#
+# These calls take a few microseconds on the GPU for a decode batch, so their checks are kept
+# cheap: one comparison per tensor where it is as expected, and the reason worked out only where
+# it is not.
+
+def _raw_stream(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _device_of(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _want(t: torch.Tensor, name: str, shape, dtype, device):
+    """t is a dense tensor of this shape (a tuple), type and CUDA device."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
+    _need(t, name, shape, dtype, device)
+
+
+def _want_view(t: torch.Tensor, name: str, shape, dtype, device):
+    """The same without the demand that it is dense."""
+    if t.dtype is dtype and t.shape == shape and t.device == device:
+        return
+    _need(t, name, shape, dtype, device, dense=False)
+
 
 def _call(device: torch.device, name: str, *args):
     """lib().<name>(*args, stream) with the tensors' device current, and its status checked."""
-    L = lib()
-    if device.index is None or torch.cuda.current_device() == device.index:
-        _check(getattr(L, name)(*args, _stream(device)), name)
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
-            _check(getattr(L, name)(*args, _stream(device)), name)
+            status = fn(*args, _raw_stream(device))
+    if status != GDN_OK:
+        _check(status, name)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _dense_from(t: torch.Tensor, name: str, dim: int, what: str) -> int:
+    """Elements of the dimensions from ``dim`` on, which must be dense."""
+    shape, strides, inner = t.shape, t.stride(), 1
+    for i in range(len(shape) - 1, dim - 1, -1):
+        if shape[i] != 1 and strides[i] != inner:
+            raise ValueError(f"{name}: {what} must be dense, got strides {strides}")
+        inner *= shape[i]
+    return inner
 
 
 def _token_rows(t: torch.Tensor, name: str, lead: int) -> int:
-    """The token stride of t [tokens.., dense..] with ``lead`` token dimensions (dense among
-    themselves) ahead of dense inner ones."""
-    inner = 1
-    for i in range(t.dim() - 1, lead - 1, -1):
-        if t.shape[i] != 1 and t.stride(i) != inner:
-            raise ValueError(f"{name}: the dimensions behind the tokens must be dense, got strides {t.stride()}")
-        inner *= t.shape[i]
-    stride, have = None, 1
-    for i in range(lead - 1, -1, -1):
-        if t.shape[i] == 1:
-            continue
-        if stride is None:
-            stride = t.stride(i)
-        elif t.stride(i) != stride * have:
-            raise ValueError(f"{name}: tokens must follow one another at one stride, got strides {t.stride()}")
-        have *= t.shape[i]
-    return inner if stride is None else stride
-
-
-def _page_stride(t: torch.Tensor, name: str, shape) -> int:
-    """The stride (elements) of pool t [P, *shape] between its dense pages."""
-    if t.dim() != len(shape) + 1 or tuple(t.shape[1:]) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [pages, {', '.join(map(str, shape))}]")
-    inner = 1
-    for i in range(t.dim() - 1, 0, -1):
-        if t.shape[i] != 1 and t.stride(i) != inner:
-            raise ValueError(f"{name}: pages must be dense, got strides {t.stride()}")
-        inner *= t.shape[i]
-    return inner if t.shape[0] <= 1 else t.stride(0)
+    """The token stride of t, whose first ``lead`` (1 or 2) dimensions count tokens that follow
+    one another at one stride; the dimensions behind them must be dense."""
+    inner = _dense_from(t, name, lead, "the dimensions behind the tokens")
+    shape, strides = t.shape, t.stride()
+    if lead == 1:
+        return inner if shape[0] <= 1 else strides[0]
+    if shape[1] <= 1:
+        return inner if shape[0] <= 1 else strides[0]
+    if shape[0] > 1 and strides[0] != strides[1] * shape[1]:
+        raise ValueError(f"{name}: tokens must follow one another at one stride, got strides {strides}")
+    return strides[1]
 
 
 def gdn_decode_paged(x: torch.Tensor, conv_w: torch.Tensor, conv_pool: torch.Tensor, state_pool: torch.Tensor,
@@ -419,74 +452,85 @@ def gdn_decode_paged(x: torch.Tensor, conv_w: torch.Tensor, conv_pool: torch.Ten
     not be read or written by another in the same call. Returns o [B, n_tok, Hv, dv]."""
     if x.dim() != 3 or state_pool.dim() != 4:
         raise ValueError("x must be [B, n_tok, Cc] and state_pool [P, Hv, dv, dk]")
+    dev, dt = _device_of(x, "x"), x.dtype
     B, n_tok, Cc = x.shape
     P, Hv, dv, dk = state_pool.shape
-    dev = x.device
     if Cc != 2 * Hk * dk + Hv * dv:
         raise ValueError(f"x has {Cc} channels, expected 2*Hk*dk + Hv*dv = {2 * Hk * dk + Hv * dv}")
-    _need(x, "x", device=dev, dense=False)
-    _need(conv_w, "conv_w", (Cc, 4), x.dtype, dev)
-    _need(conv_pool, "conv_pool", (P, 3, Cc), x.dtype, dev, dense=False)
-    _need(state_pool, "state_pool", device=dev, dense=False)
-    _need(read_pages, "read_pages", (B,), torch.int32, dev)
-    _need(write_pages, "write_pages", (B, n_tok), torch.int32, dev)
-    _need(n_valid, "n_valid", (B,), torch.int32, dev)
-    _need(g, "g", (B, n_tok, Hv), torch.float32, dev)
-    _need(beta, "beta", (B, n_tok, Hv), torch.float32, dev)
-    _need(z, "z", (B, n_tok, Hv, dv), x.dtype, dev, dense=False)
-    _need(norm_w, "norm_w", (dv,), x.dtype, dev)
+    f32, i32 = torch.float32, torch.int32
+    _want(conv_w, "conv_w", (Cc, 4), dt, dev)
+    _want_view(conv_pool, "conv_pool", (P, 3, Cc), dt, dev)
+    _want_view(state_pool, "state_pool", (P, Hv, dv, dk), state_pool.dtype, dev)
+    _want(read_pages, "read_pages", (B,), i32, dev)
+    _want(g, "g", (B, n_tok, Hv), f32, dev)
+    _want(beta, "beta", (B, n_tok, Hv), f32, dev)
+    if write_pages is not None:
+        _want(write_pages, "write_pages", (B, n_tok), i32, dev)
+    if n_valid is not None:
+        _want(n_valid, "n_valid", (B,), i32, dev)
     if (z is None) != (norm_w is None):
         raise ValueError("z and norm_w come together")
+    z_stride = 0
+    if z is not None:
+        _want_view(z, "z", (B, n_tok, Hv, dv), dt, dev)
+        _want(norm_w, "norm_w", (dv,), dt, dev)
+        z_stride = _token_rows(z, "z", 2)
     if o is None:
-        o = torch.empty((B, n_tok, Hv, dv), dtype=x.dtype, device=dev)
-    _need(o, "o", (B, n_tok, Hv, dv), x.dtype, dev)
-    _call(dev, "gdn_decode_paged", _ptr(x), _token_rows(x, "x", 2), _ptr(conv_w), _ptr(conv_pool),
-          _page_stride(conv_pool, "conv_pool", (3, Cc)), _ptr(state_pool),
-          _page_stride(state_pool, "state_pool", (Hv, dv, dk)), _dtype_code(state_pool), P, _ptr(read_pages),
-          _ptr(write_pages), _ptr(n_valid), _ptr(g), _ptr(beta), _ptr(z), 0 if z is None else _token_rows(z, "z", 2),
-          _ptr(norm_w), float(eps), _ptr(o), _dtype_code(x), B, n_tok, Hk, Hv, dk, dv, float(scale))
+        o = torch.empty((B, n_tok, Hv, dv), dtype=dt, device=dev)
+    else:
+        _want(o, "o", (B, n_tok, Hv, dv), dt, dev)
+    taps = _dense_from(conv_pool, "conv_pool", 1, "pages")
+    page = _dense_from(state_pool, "state_pool", 1, "pages")
+    _call(dev, "gdn_decode_paged", x.data_ptr(), _token_rows(x, "x", 2), conv_w.data_ptr(), conv_pool.data_ptr(),
+          taps if P <= 1 else conv_pool.stride(0), state_pool.data_ptr(), page if P <= 1 else state_pool.stride(0),
+          _dtype_code(state_pool), P, read_pages.data_ptr(), _addr(write_pages), _addr(n_valid), g.data_ptr(),
+          beta.data_ptr(), _addr(z), z_stride, _addr(norm_w), eps, o.data_ptr(), _dtype_code(x), B, n_tok, Hk, Hv,
+          dk, dv, scale)
     return o
 
 
 def _pool_layout(t: torch.Tensor, name: str, page_dim: int):
-    """(pages, page stride, layers, layer stride, page bytes) in bytes of a pool [P, page..]
+    """(pages, layers, page bytes, page stride, layer stride) in bytes of a pool [P, page..]
     (page_dim 0) or [layers, P, page..] (page_dim 1)."""
-    if page_dim not in (0, 1):
-        raise ValueError(f"page_dim must be 0 or 1, got {page_dim}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() < page_dim + 2:
         raise ValueError(f"{name} has {t.dim()} dimensions, too few for page_dim = {page_dim}")
-    es, inner = t.element_size(), 1
-    for i in range(t.dim() - 1, page_dim, -1):
-        if t.shape[i] != 1 and t.stride(i) != inner:
-            raise ValueError(f"{name}: pages must be dense, got strides {t.stride()}")
-        inner *= t.shape[i]
-    pages, layers = t.shape[page_dim], t.shape[0] if page_dim else 1
-    return (pages, t.stride(page_dim) * es if pages > 1 else inner * es, layers,
-            t.stride(0) * es if layers > 1 else 0, inner * es)
+    es, shape, strides = t.element_size(), t.shape, t.stride()
+    page = _dense_from(t, name, page_dim + 1, "pages") * es
+    pages, layers = shape[page_dim], shape[0] if page_dim else 1
+    return pages, layers, page, strides[page_dim] * es if pages > 1 else page, strides[0] * es if layers > 1 else 0
 
 
-def gdn_pages_copy(src_pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
-                   dst_pool: Optional[torch.Tensor] = None, page_dim: int = 0) -> None:
+def gdn_pages_copy(src_pool, src: torch.Tensor, dst: torch.Tensor, dst_pool=None, page_dim: int = 0) -> None:
     """Page src[i] of ``src_pool`` to page dst[i] of ``dst_pool`` (default: the same pool) for
     every entry of the int32 lists, as if all were read before any is written; the last entry of
     a repeated destination counts, entries that are not pages are skipped. Pools are [P, page..],
-    or [layers, P, page..] with ``page_dim`` = 1 (every layer is copied)."""
-    dev = src_pool.device
-    dst_pool = src_pool if dst_pool is None else dst_pool
-    sp, ss, layers, sl, bytes_ = _pool_layout(src_pool, "src_pool", page_dim)
-    dp, ds, d_layers, dl, d_bytes = _pool_layout(dst_pool, "dst_pool", page_dim)
-    if dst_pool.device != dev or dst_pool.dtype != src_pool.dtype or d_layers != layers or d_bytes != bytes_:
-        raise ValueError("src_pool and dst_pool must agree in device, dtype, layers and page size")
-    _need(src, "src", (src.numel(),), torch.int32, dev)
-    _need(dst, "dst", (src.numel(),), torch.int32, dev)
-    _call(dev, "gdn_pages_copy", _ptr(src_pool), ss, sl, sp, _ptr(dst_pool), ds, dl, dp, bytes_, layers,
-          _ptr(src), _ptr(dst), src.numel())
-
-
-def _need_refs(refs: torch.Tensor):
-    _need(refs, "refs", (refs.numel(),), torch.int32)
+    or [layers, P, page..] with ``page_dim`` = 1 (every layer is copied); a list of up to four
+    pools with equal P is copied by one call."""
+    if page_dim not in (0, 1):
+        raise ValueError(f"page_dim must be 0 or 1, got {page_dim}")
+    froms = [src_pool] if isinstance(src_pool, torch.Tensor) else list(src_pool)
+    tos = froms if dst_pool is None else [dst_pool] if isinstance(dst_pool, torch.Tensor) else list(dst_pool)
+    if not 1 <= len(froms) <= 4 or len(tos) != len(froms):
+        raise ValueError(f"expected 1 to 4 pools and as many destinations, got {len(froms)} and {len(tos)}")
+    dev = _device_of(froms[0], "src_pool")
+    desc = (_PagePool * len(froms))()
+    sp = dp = None
+    for d, a, b in zip(desc, froms, tos):
+        pages, layers, size, stride, layer = _pool_layout(a, "src_pool", page_dim)
+        d.src, d.page_bytes, d.src_page_stride, d.src_layer_stride, d.layers = a.data_ptr(), size, stride, layer, layers
+        to_pages = pages
+        if b is not a:
+            to_pages, to_layers, to_size, stride, layer = _pool_layout(b, "dst_pool", page_dim)
+            if b.dtype != a.dtype or to_layers != layers or to_size != size:
+                raise ValueError("source and destination pools must agree in dtype, layers and page size")
+        d.dst, d.dst_page_stride, d.dst_layer_stride = b.data_ptr(), stride, layer
+        if a.device != dev or b.device != dev or sp not in (None, pages) or dp not in (None, to_pages):
+            raise ValueError("all pools must be on one device and agree in their number of pages")
+        sp, dp = pages, to_pages
+    n = src.numel()
+    _want(src, "src", (n,), torch.int32, dev)
+    _want(dst, "dst", (n,), torch.int32, dev)
+    _call(dev, "gdn_pages_copy", ctypes.addressof(desc), len(froms), sp, dp, src.data_ptr(), dst.data_ptr(), n)
 
 
 def gdn_pages_take(refs: torch.Tensor, n: Optional[int] = None, src: Optional[torch.Tensor] = None,
@@ -495,22 +539,26 @@ def gdn_pages_take(refs: torch.Tensor, n: Optional[int] = None, src: Optional[to
     them, or one for each entry of ``src`` that is a page. Returns them (int32, -1: none)."""
     if (n is None) == (src is None):
         raise ValueError("give either n or src")
-    _need_refs(refs)
-    n = src.numel() if n is None else n
-    _need(src, "src", (n,), torch.int32, refs.device)
+    dev, P = _device_of(refs, "refs"), refs.numel()
+    _want(refs, "refs", (P,), torch.int32, dev)
+    if src is not None:
+        n = src.numel()
+        _want(src, "src", (n,), torch.int32, dev)
     if out is None:
-        out = torch.empty((n,), dtype=torch.int32, device=refs.device)
-    _need(out, "out", (n,), torch.int32, refs.device)
-    _call(refs.device, "gdn_pages_take", _ptr(refs), refs.numel(), _ptr(src), n, _ptr(out))
+        out = torch.empty((n,), dtype=torch.int32, device=dev)
+    else:
+        _want(out, "out", (n,), torch.int32, dev)
+    _call(dev, "gdn_pages_take", refs.data_ptr(), P, _addr(src), n, out.data_ptr())
     return out
 
 
 def gdn_pages_ref(refs: torch.Tensor, pages: torch.Tensor, delta: int) -> None:
     """refs[p] += delta for every entry p of ``pages`` that is a page, not below 0: 1 shares
     pages, -1 frees them."""
-    _need_refs(refs)
-    _need(pages, "pages", (pages.numel(),), torch.int32, refs.device)
-    _call(refs.device, "gdn_pages_ref", _ptr(refs), refs.numel(), _ptr(pages), pages.numel(), int(delta))
+    dev, P, n = _device_of(refs, "refs"), refs.numel(), pages.numel()
+    _want(refs, "refs", (P,), torch.int32, dev)
+    _want(pages, "pages", (n,), torch.int32, dev)
+    _call(dev, "gdn_pages_ref", refs.data_ptr(), P, pages.data_ptr(), n, int(delta))
 
 
 def gdn_pages_fork(refs: torch.Tensor, src: torch.Tensor, pools, page_dim: int = 0,
@@ -518,21 +566,22 @@ def gdn_pages_fork(refs: torch.Tensor, src: torch.Tensor, pools, page_dim: int =
     """A new page for each entry of ``src`` (see ``gdn_pages_take``), holding a copy of page
     src[i] in each pool of ``pools``. Returns the new pages."""
     out = gdn_pages_take(refs, src=src, out=out)
-    for pool in pools:
-        gdn_pages_copy(pool, src, out, page_dim=page_dim)
+    gdn_pages_copy(pools, src, out, page_dim=page_dim)
     return out
 
 
 def gdn_pages_plan(refs: torch.Tensor, table: Optional[torch.Tensor] = None):
     """The moves that bring the live pages (count > 0) to the front: (src, dst, map, n_live), the
     lists padded with -1; refs and the page numbers in ``table`` (any shape) are rewritten."""
-    _need_refs(refs)
-    P, dev = refs.numel(), refs.device
-    _need(table, "table", dtype=torch.int32, device=dev)
-    new = lambda n: torch.empty((n,), dtype=torch.int32, device=dev)  # noqa: E731
-    src, dst, new_of, n_live = new(P // 2), new(P // 2), new(P), new(1)
-    _call(dev, "gdn_pages_plan", _ptr(refs), P, _ptr(table), 0 if table is None else table.numel(),
-          _ptr(src), _ptr(dst), _ptr(new_of), _ptr(n_live))
+    dev, P = _device_of(refs, "refs"), refs.numel()
+    _want(refs, "refs", (P,), torch.int32, dev)
+    if table is not None:
+        _want(table, "table", table.shape, torch.int32, dev)
+    half = P // 2
+    lists = torch.empty((2 * half + P + 1,), dtype=torch.int32, device=dev)
+    src, dst, new_of, n_live = lists[:half], lists[half:2 * half], lists[2 * half:-1], lists[-1:]
+    _call(dev, "gdn_pages_plan", refs.data_ptr(), P, _addr(table), 0 if table is None else table.numel(),
+          src.data_ptr(), dst.data_ptr(), new_of.data_ptr(), n_live.data_ptr())
     return src, dst, new_of, n_live
 
 
@@ -543,18 +592,9 @@ def gdn_pages_compact(refs: torch.Tensor, table: Optional[torch.Tensor], pools, 
     """Bring the live pages to the front of every pool: ``refs`` and ``table`` are rewritten.
     Returns (map [P]: each live page's new place, -1 for free ones; n_live [1]), on the device."""
     src, dst, new_of, n_live = gdn_pages_plan(refs, table)
-    for pool in pools:
-        for i in range(0, src.numel(), _MAX_LIST):
-            gdn_pages_copy(pool, src[i:i + _MAX_LIST], dst[i:i + _MAX_LIST], page_dim=page_dim)
+    for i in range(0, src.numel(), _MAX_LIST):
+        gdn_pages_copy(pools, src[i:i + _MAX_LIST], dst[i:i + _MAX_LIST], page_dim=page_dim)
     return new_of, n_live
-
-
-def _norm_workspace(D: int, workspace: Optional[torch.Tensor], device):
-    need = lib().gdn_norm_bwd_workspace_size(D)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    _need(workspace, "workspace", device=device)
-    return workspace, workspace.numel() * workspace.element_size()
 
 
 def gdn_norm_bwd_workspace_size(D: int) -> int:
@@ -562,19 +602,28 @@ def gdn_norm_bwd_workspace_size(D: int) -> int:
     return int(lib().gdn_norm_bwd_workspace_size(D))
 
 
+def _norm_workspace(D: int, workspace: Optional[torch.Tensor], device):
+    if workspace is None:
+        need = lib().gdn_norm_bwd_workspace_size(D)
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    _need(workspace, "workspace", device=device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
 def gdn_gated_norm(o: torch.Tensor, z: torch.Tensor, w: torch.Tensor, eps: float = 1e-6,
                    y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """o / sqrt(mean(o^2) + eps) * w * SiLU(z) over the last dimension: o [T, Hv, dv], z the same
     (tokens may be strided), w [dv]. ``y`` may be ``o``."""
-    T, Hv, dv = o.shape
-    dev = o.device
-    _need(o, "o", device=dev)
-    _need(z, "z", (T, Hv, dv), o.dtype, dev, dense=False)
-    _need(w, "w", (dv,), o.dtype, dev)
+    dev, dt, shape = _device_of(o, "o"), o.dtype, o.shape
+    T, Hv, dv = shape
+    _want(o, "o", shape, dt, dev)
+    _want_view(z, "z", shape, dt, dev)
+    _want(w, "w", (dv,), dt, dev)
     if y is None:
         y = torch.empty_like(o)
-    _need(y, "y", (T, Hv, dv), o.dtype, dev)
-    _call(dev, "gdn_gated_norm", _ptr(o), _ptr(z), _token_rows(z, "z", 1), _ptr(w), float(eps), _ptr(y),
+    else:
+        _want(y, "y", shape, dt, dev)
+    _call(dev, "gdn_gated_norm", o.data_ptr(), z.data_ptr(), _token_rows(z, "z", 1), w.data_ptr(), eps, y.data_ptr(),
           _dtype_code(o), T, Hv, dv)
     return y
 
@@ -584,21 +633,22 @@ def gdn_gated_norm_bwd(o: torch.Tensor, z: torch.Tensor, w: torch.Tensor, dy: to
                        dw: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """Backward of ``gdn_gated_norm``: (do, dz, dw [dv] fp32). ``do`` may be ``dy``; ``dz`` may be
     a token-strided view."""
-    T, Hv, dv = o.shape
-    dev = o.device
-    _need(o, "o", device=dev)
-    _need(z, "z", (T, Hv, dv), o.dtype, dev, dense=False)
-    _need(w, "w", (dv,), o.dtype, dev)
-    _need(dy, "dy", (T, Hv, dv), o.dtype, dev)
+    dev, dt, shape = _device_of(o, "o"), o.dtype, o.shape
+    T, Hv, dv = shape
     do = torch.empty_like(o) if do is None else do
-    dz = torch.empty((T, Hv, dv), dtype=o.dtype, device=dev) if dz is None else dz
+    dz = torch.empty(shape, dtype=dt, device=dev) if dz is None else dz
     dw = torch.empty((dv,), dtype=torch.float32, device=dev) if dw is None else dw
-    _need(do, "do", (T, Hv, dv), o.dtype, dev)
-    _need(dz, "dz", (T, Hv, dv), o.dtype, dev, dense=False)
-    _need(dw, "dw", (dv,), torch.float32, dev)
+    _want(o, "o", shape, dt, dev)
+    _want_view(z, "z", shape, dt, dev)
+    _want(w, "w", (dv,), dt, dev)
+    _want(dy, "dy", shape, dt, dev)
+    _want(do, "do", shape, dt, dev)
+    _want_view(dz, "dz", shape, dt, dev)
+    _want(dw, "dw", (dv,), torch.float32, dev)
     workspace, ws_bytes = _norm_workspace(dv, workspace, dev)
-    _call(dev, "gdn_gated_norm_bwd", _ptr(o), _ptr(z), _token_rows(z, "z", 1), _ptr(w), float(eps), _ptr(dy),
-          _ptr(do), _ptr(dz), _token_rows(dz, "dz", 1), _ptr(dw), _dtype_code(o), T, Hv, dv, _ptr(workspace), ws_bytes)
+    _call(dev, "gdn_gated_norm_bwd", o.data_ptr(), z.data_ptr(), _token_rows(z, "z", 1), w.data_ptr(), eps,
+          dy.data_ptr(), do.data_ptr(), dz.data_ptr(), _token_rows(dz, "dz", 1), dw.data_ptr(), _dtype_code(o), T, Hv,
+          dv, workspace.data_ptr(), ws_bytes)
     return do, dz, dw
 
 
@@ -607,17 +657,17 @@ def gdn_add_norm(x: torch.Tensor, residual: torch.Tensor, w: torch.Tensor, scale
     """h = residual + scale * x and its norm n = h / sqrt(mean(h^2) + eps) * (w + w_add), over the
     last of two dimensions. h has the residual's dtype and may be ``residual``; n has x's.
     Returns (n, h)."""
-    T, D = x.shape
-    dev = x.device
-    _need(x, "x", device=dev)
-    _need(residual, "residual", (T, D), None, dev)
-    _need(w, "w", (D,), x.dtype, dev)
+    dev, dt, shape, res = _device_of(x, "x"), x.dtype, x.shape, residual.dtype
+    T, D = shape
     h = torch.empty_like(residual) if h is None else h
     n = torch.empty_like(x) if n is None else n
-    _need(h, "h", (T, D), residual.dtype, dev)
-    _need(n, "n", (T, D), x.dtype, dev)
-    _call(dev, "gdn_add_norm", _ptr(x), _ptr(residual), _ptr(w), float(scale), float(w_add), float(eps), _ptr(h),
-          _dtype_code(residual), _ptr(n), _dtype_code(x), T, D)
+    _want(x, "x", shape, dt, dev)
+    _want(residual, "residual", shape, res, dev)
+    _want(w, "w", (D,), dt, dev)
+    _want(h, "h", shape, res, dev)
+    _want(n, "n", shape, dt, dev)
+    _call(dev, "gdn_add_norm", x.data_ptr(), residual.data_ptr(), w.data_ptr(), scale, w_add, eps, h.data_ptr(),
+          _dtype_code(residual), n.data_ptr(), _dtype_code(x), T, D)
     return n, h
 
 
@@ -628,19 +678,21 @@ def gdn_add_norm_bwd(h: torch.Tensor, w: torch.Tensor, dn: torch.Tensor, dh: Opt
     """Backward of ``gdn_add_norm`` at the h it stored: from dn and dh (the gradient that reaches
     h on its own way, or None) the gradients (dx, dres, dw [D] fp32) of x, the residual and w.
     ``dres`` may be ``dh``; dx has dn's dtype (x, w, n and dx share it)."""
-    T, D = h.shape
-    dev = h.device
-    _need(h, "h", device=dev)
-    _need(w, "w", (D,), dn.dtype, dev)
-    _need(dn, "dn", (T, D), None, dev)
-    _need(dh, "dh", (T, D), h.dtype, dev)
+    dev, dt, shape, res = _device_of(h, "h"), dn.dtype, h.shape, h.dtype
+    T, D = shape
     dres = torch.empty_like(h) if dres is None else dres
     dx = torch.empty_like(dn) if dx is None else dx
     dw = torch.empty((D,), dtype=torch.float32, device=dev) if dw is None else dw
-    _need(dres, "dres", (T, D), h.dtype, dev)
-    _need(dx, "dx", (T, D), dn.dtype, dev)
-    _need(dw, "dw", (D,), torch.float32, dev)
+    _want(h, "h", shape, res, dev)
+    _want(w, "w", (D,), dt, dev)
+    _want(dn, "dn", shape, dt, dev)
+    if dh is not None:
+        _want(dh, "dh", shape, res, dev)
+    _want(dres, "dres", shape, res, dev)
+    _want(dx, "dx", shape, dt, dev)
+    _want(dw, "dw", (D,), torch.float32, dev)
     workspace, ws_bytes = _norm_workspace(D, workspace, dev)
-    _call(dev, "gdn_add_norm_bwd", _ptr(h), _ptr(w), _ptr(dn), _ptr(dh), float(scale), float(w_add), float(eps),
-          _ptr(dres), _dtype_code(h), _ptr(dx), _ptr(dw), _dtype_code(dn), T, D, _ptr(workspace), ws_bytes)
+    _call(dev, "gdn_add_norm_bwd", h.data_ptr(), w.data_ptr(), dn.data_ptr(), _addr(dh), scale, w_add, eps,
+          dres.data_ptr(), _dtype_code(h), dx.data_ptr(), dw.data_ptr(), _dtype_code(dn), T, D, workspace.data_ptr(),
+          ws_bytes)
     return dx, dres, dw

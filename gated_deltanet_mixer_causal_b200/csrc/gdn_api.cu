@@ -446,39 +446,49 @@ gdn_status_t gdn_decode_paged(const void* x, int64_t x_stride, const void* conv_
                      "decode_paged launch");
 }
 
-gdn_status_t gdn_pages_copy(const void* src_pool, int64_t src_page_stride, int64_t src_layer_stride,
-                            int32_t src_pages, void* dst_pool, int64_t dst_page_stride,
-                            int64_t dst_layer_stride, int32_t dst_pages, int64_t page_bytes,
-                            int32_t layers, const int32_t* src, const int32_t* dst, int32_t n,
+gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32_t src_pages,
+                            int32_t dst_pages, const int32_t* src, const int32_t* dst, int32_t n,
                             gdn_stream_t stream) {
-  if (n < 0 || src_pages < 0 || dst_pages < 0 || layers < 0)
-    return fail(GDN_ERR_INVALID_ARG, "pages_copy: negative count");
-  if (page_bytes <= 0 || page_bytes % 16)
-    return fail(GDN_ERR_INVALID_ARG, "pages_copy: page_bytes = %lld must be a positive multiple of 16", (long long)page_bytes);
-  if (src_page_stride == 0) src_page_stride = page_bytes;
-  if (dst_page_stride == 0) dst_page_stride = page_bytes;
-  if (!pages_apart(src_pages, src_page_stride, layers, src_layer_stride, page_bytes) ||
-      !pages_apart(dst_pages, dst_page_stride, layers, dst_layer_stride, page_bytes))
-    return fail(GDN_ERR_INVALID_ARG, "pages_copy: strides must be multiples of 16 bytes that keep the pages apart");
+  if (n < 0 || src_pages < 0 || dst_pages < 0) return fail(GDN_ERR_INVALID_ARG, "pages_copy: negative count");
+  if (n_pools < 1 || n_pools > gdn::kPagesMaxPools || !pools)
+    return fail(GDN_ERR_INVALID_ARG, "pages_copy: %d pools, expected 1 to %d", n_pools, gdn::kPagesMaxPools);
   if (n > gdn::kPagesMaxList)
     return fail(GDN_ERR_UNSUPPORTED, "pages_copy: %d entries, at most %d a call", n, gdn::kPagesMaxList);
-  if (n == 0 || layers == 0 || src_pages == 0 || dst_pages == 0) return ok();
-  if (!src_pool || !dst_pool || !src || !dst)
-    return fail(GDN_ERR_INVALID_ARG, "pages_copy: pools and lists must be non-null");
-  if (!aligned16(src_pool) || !aligned16(dst_pool) || !aligned4(src) || !aligned4(dst))
-    return fail(GDN_ERR_INVALID_ARG, "pages_copy: pools must be 16-byte aligned, lists 4-byte aligned");
-  const size_t sb = (size_t)((layers - 1) * src_layer_stride + (src_pages - 1) * src_page_stride + page_bytes);
-  const size_t db = (size_t)((layers - 1) * dst_layer_stride + (dst_pages - 1) * dst_page_stride + page_bytes);
-  if (src_pool == dst_pool) {
-    if (src_pages != dst_pages || src_page_stride != dst_page_stride || (layers > 1 && src_layer_stride != dst_layer_stride))
+  gdn::PagesCopy a{};
+  a.src_pages = src_pages; a.dst_pages = dst_pages; a.src = src; a.dst = dst; a.n = n;
+  size_t db[gdn::kPagesMaxPools] = {}, sb[gdn::kPagesMaxPools] = {};
+  for (int i = 0; i < n_pools; ++i) {
+    gdn_page_pool_t p = pools[i];
+    if (p.page_bytes <= 0 || p.page_bytes % 16)
+      return fail(GDN_ERR_INVALID_ARG, "pages_copy: page_bytes = %lld must be a positive multiple of 16", (long long)p.page_bytes);
+    if (p.layers < 0) return fail(GDN_ERR_INVALID_ARG, "pages_copy: negative count");
+    if (p.src_page_stride == 0) p.src_page_stride = p.page_bytes;
+    if (p.dst_page_stride == 0) p.dst_page_stride = p.page_bytes;
+    if (!pages_apart(src_pages, p.src_page_stride, p.layers, p.src_layer_stride, p.page_bytes) ||
+        !pages_apart(dst_pages, p.dst_page_stride, p.layers, p.dst_layer_stride, p.page_bytes))
+      return fail(GDN_ERR_INVALID_ARG, "pages_copy: strides must be multiples of 16 bytes that keep the pages apart");
+    if (n == 0 || p.layers == 0 || src_pages == 0 || dst_pages == 0) continue;
+    if (!p.src || !p.dst || !src || !dst)
+      return fail(GDN_ERR_INVALID_ARG, "pages_copy: pools and lists must be non-null");
+    if (!aligned16(p.src) || !aligned16(p.dst) || !aligned4(src) || !aligned4(dst))
+      return fail(GDN_ERR_INVALID_ARG, "pages_copy: pools must be 16-byte aligned, lists 4-byte aligned");
+    sb[i] = (size_t)((p.layers - 1) * p.src_layer_stride + (src_pages - 1) * p.src_page_stride + p.page_bytes);
+    db[i] = (size_t)((p.layers - 1) * p.dst_layer_stride + (dst_pages - 1) * p.dst_page_stride + p.page_bytes);
+    const bool same = p.src == p.dst;
+    if (same && (src_pages != dst_pages || p.src_page_stride != p.dst_page_stride ||
+                 (p.layers > 1 && p.src_layer_stride != p.dst_layer_stride)))
       return fail(GDN_ERR_INVALID_ARG, "pages_copy: one pool, but different strides or page counts");
-  } else if (overlap(src_pool, sb, dst_pool, db)) {
-    return fail(GDN_ERR_INVALID_ARG, "pages_copy: the pools overlap");
+    if (!same && overlap(p.src, sb[i], p.dst, db[i])) return fail(GDN_ERR_INVALID_ARG, "pages_copy: the pools overlap");
+    if (overlap(src, (size_t)n * 4, p.dst, db[i]) || overlap(dst, (size_t)n * 4, p.dst, db[i]))
+      return fail(GDN_ERR_INVALID_ARG, "pages_copy: a list overlaps a destination pool");
+    for (int j = 0; j < i; ++j)
+      if (overlap(p.dst, db[i], pools[j].dst, db[j]) || overlap(p.dst, db[i], pools[j].src, sb[j]) ||
+          overlap(p.src, sb[i], pools[j].dst, db[j]))
+        return fail(GDN_ERR_INVALID_ARG, "pages_copy: the pools overlap");
+    a.pool[a.n_pools++] = {(const char*)p.src, (char*)p.dst, p.page_bytes, p.src_page_stride, p.src_layer_stride,
+                           p.dst_page_stride, p.dst_layer_stride, p.layers, same};
   }
-  if (overlap(src, (size_t)n * 4, dst_pool, db) || overlap(dst, (size_t)n * 4, dst_pool, db))
-    return fail(GDN_ERR_INVALID_ARG, "pages_copy: a list overlaps the destination pool");
-  gdn::PagesCopy a{(const char*)src_pool, (char*)dst_pool, page_bytes, src_page_stride, dst_page_stride,
-                   src_layer_stride, dst_layer_stride, src_pages, dst_pages, layers, src, dst, n};
+  if (a.n_pools == 0) return ok();
   return cuda_status(gdn::launch_pages_copy(a, (cudaStream_t)stream), "pages_copy launch");
 }
 

@@ -87,10 +87,16 @@ cudaError_t launch_decode_paged(int dtype, int state_dtype, int d, const PagedDe
 
 // Page copies: strides in bytes; every page a multiple of 16 bytes.
 constexpr int kPagesMaxList = 2048;
+constexpr int kPagesMaxPools = 4;
+struct PagePool {
+  const char* src; char* dst;
+  int64_t page_bytes, src_page, src_layer, dst_page, dst_layer;
+  int32_t layers;
+  bool same;                                // src and dst are one pool
+};
 struct PagesCopy {
-  const char* src_pool; char* dst_pool;
-  int64_t page_bytes, src_page, dst_page, src_layer, dst_layer;
-  int32_t src_pages, dst_pages, layers;
+  PagePool pool[kPagesMaxPools]; int32_t n_pools;
+  int32_t src_pages, dst_pages;
   const int32_t* src; const int32_t* dst; int32_t n;
 };
 cudaError_t launch_pages_copy(const PagesCopy& a, cudaStream_t stream);

@@ -3,6 +3,7 @@
 // A page holds one sequence's state (or its conv taps) of one layer. A copy moves whole pages,
 // so it is bound by HBM: 2 x page bytes for each entry. The lists, counts and plans are a few
 // ints per page and run in one CTA.
+#include <stdlib.h>
 #include "common.cuh"
 #include "launch.h"
 
@@ -72,8 +73,8 @@ pages_copy_kernel(const PagesCopy a, uint32_t slots) {
   Table tab{sm, sm + slots, slots - 1};
   int32_t* ms = sm + 2 * slots;       // [n] sources of the entries that count
   int32_t* md = ms + a.n;             // [n] their destinations
-  __shared__ int clash, sums[32];
-  if (threadIdx.x == 0) clash = 0;
+  __shared__ int sums[32], chained;
+  if (threadIdx.x == 0) chained = 0;
   for (uint32_t s = threadIdx.x; s < slots; s += kCopyThreads) { tab.key[s] = -1; tab.val[s] = -1; }
   __syncthreads();
   auto counts = [&](int i, int32_t& s, int32_t& d) {
@@ -92,54 +93,65 @@ pages_copy_kernel(const PagesCopy a, uint32_t slots) {
     atomicMax(&tab.val[h], i);
   }
   __syncthreads();
-  const bool same = a.src_pool == a.dst_pool;
   // the entries that count, in the list's order: every CTA must number them alike
   int m = 0;
   for (int i0 = 0; i0 < a.n; i0 += kCopyThreads) {
     const int i = i0 + threadIdx.x;
     int32_t s = -1, d = -1;
-    const bool on = i < a.n && counts(i, s, d) && find(tab, d) == i && !(same && s == d);
+    const bool on = i < a.n && counts(i, s, d) && find(tab, d) == i;
     int total;
     const int at = m + block_scan<kCopyThreads / 32>(on, sums, total);
     if (on) {
       ms[at] = s; md[at] = d;
-      if (same && find(tab, s) >= 0) clash = 1;
+      if (s != d && find(tab, s) >= 0) chained = 1;
     }
     m += total;
   }
   __syncthreads();
   if (m == 0) return;
 
-  // the tile: mm entries x w bytes, mm w = the CTA's registers
-  constexpr int64_t kTile = (int64_t)kCopyThreads * U * 16;
-  int64_t w = 16;
-  if (clash) {
-    while (w * 2 * m <= kTile) w *= 2;
-  } else {
-    while (w < a.page_bytes && w < kTile) w *= 2;
-  }
-  const int mm = (int)(kTile / w), units = (int)(w / 16);
-  const int64_t cols = (a.page_bytes + w - 1) / w, groups = (m + mm - 1) / mm;
-  const int64_t tiles = cols * groups * a.layers;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t grp = tile % groups, rest = tile / groups;
-    const int64_t col = (rest % cols) * w, layer = rest / cols;
-    uint4 v[U];
-    char* to[U];
+  constexpr int kLog = U == 8 ? 16 : U == 4 ? 15 : 14;             // bytes of a tile, a power of two
+  static_assert(kCopyThreads * U * 16 == 1 << kLog, "");
+  int64_t first = 0;                                               // this pool's first tile
+  for (int k = 0; k < a.n_pools; ++k) {
+    const PagePool p = a.pool[k];
+    // the tile: 2^lm entries x 2^lw bytes
+    const bool clash = p.same && chained;
+    int lw;
+    if (clash) {
+      for (lw = kLog; lw > 4 && ((int64_t)m << lw) > (1 << kLog);) --lw;
+    } else {
+      for (lw = 4; (1LL << lw) < p.page_bytes && lw < kLog;) ++lw;
+    }
+    const int lm = kLog - lw, lu = lw - 4;
+    const int64_t cols = (p.page_bytes + (1LL << lw) - 1) >> lw, groups = (m + (1LL << lm) - 1) >> lm;
+    const int64_t tiles = cols * groups * p.layers;
+    int64_t tile = (int64_t)blockIdx.x - first % gridDim.x;        // tiles of all pools in one round
+    if (tile < 0) tile += gridDim.x;
+    first += tiles;
+    for (; tile < tiles; tile += gridDim.x) {
+      const int64_t rest = tile / groups, grp = tile - rest * groups;
+      const int64_t layer = rest / cols, col = (rest - layer * cols) << lw;
+      const char* from = p.src + layer * p.src_layer + col;
+      char* to = p.dst + layer * p.dst_layer + col;
+      uint4 v[U];
+      int32_t e[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int idx = u * kCopyThreads + threadIdx.x;
-      const int64_t e = grp * mm + idx / units, off = col + (int64_t)(idx % units) * 16;
-      to[u] = nullptr;
-      if (e < m && off < a.page_bytes) {
-        to[u] = a.dst_pool + layer * a.dst_layer + (int64_t)md[e] * a.dst_page + off;
-        v[u] = *reinterpret_cast<const uint4*>(a.src_pool + layer * a.src_layer + (int64_t)ms[e] * a.src_page + off);
+      for (int u = 0; u < U; ++u) {
+        const int idx = u * kCopyThreads + threadIdx.x;
+        const int off = (idx & ((1 << lu) - 1)) << 4;
+        const int64_t at = (grp << lm) + (idx >> lu);
+        e[u] = at < m && col + off < p.page_bytes ? (int32_t)at : -1;
+        if (e[u] >= 0 && p.same && ms[at] == md[at]) e[u] = -1;
+        if (e[u] >= 0) v[u] = __ldcs(reinterpret_cast<const uint4*>(from + (int64_t)ms[at] * p.src_page + off));
+      }
+      if (clash) __syncthreads();
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int off = ((u * kCopyThreads + threadIdx.x) & ((1 << lu) - 1)) << 4;
+        if (e[u] >= 0) __stcs(reinterpret_cast<uint4*>(to + (int64_t)md[e[u]] * p.dst_page + off), v[u]);
       }
     }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (to[u]) *reinterpret_cast<uint4*>(to[u]) = v[u];
   }
 }
 
@@ -249,7 +261,8 @@ cudaError_t launch_pages_copy(const PagesCopy& a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  return launch_copy<4>(a, sms, st);
+  if (getenv("PG_U")) { int u = atoi(getenv("PG_U")); return u == 2 ? launch_copy<2>(a, sms, st) : u == 4 ? launch_copy<4>(a, sms, st) : launch_copy<8>(a, sms, st); }
+  return launch_copy<8>(a, sms, st);
 }
 
 cudaError_t launch_pages_take(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n, int32_t* out,

@@ -384,28 +384,35 @@ gdn_status_t gdn_decode_paged(const void* x, int64_t x_stride, const void* conv_
                               int32_t Hv, int32_t dk, int32_t dv, float scale, gdn_stream_t stream);
 
 /*
- * gdn_pages_copy -- page src[i] of one pool to page dst[i] of another, or of the same pool, for
- * each of n entries and in every layer.
+ * gdn_pages_copy -- page src[i] to page dst[i] of a pool (or of another pool), for each of n
+ * entries, in every layer of each of n_pools pools that share the lists (the states and the taps).
  *
  * The result is as if every source were read before any destination is written, so one call may
  * permute the pages of a pool (the reordering of beams) or fill many from one (a fork). Where
  * several entries name one destination the last of them counts. An entry whose source or
  * destination is not a page of its pool is skipped.
  *
- * src_pool, dst_pool  page p of layer l at pool + l*layer_stride + p*page_stride (bytes, all
- *              multiples of 16; page_stride 0 means page_bytes). Pages hold any type. They must
- *              not overlap one another; the pools are either the same one (equal pointers,
- *              strides and page counts) or do not overlap.
- * page_bytes   a positive multiple of 16.
+ * pools        host array of n_pools (1 .. 4) descriptions, read during the call: page p of layer l
+ *              at src (or dst) + l*layer_stride + p*page_stride (bytes, all multiples of 16;
+ *              page_stride 0 means page_bytes). Pages hold any type; page_bytes is a positive
+ *              multiple of 16. The pages of a pool must not overlap one another; src and dst are
+ *              either the same pool (equal pointers and strides, src_pages = dst_pages) or do not
+ *              overlap, and no two of the destinations overlap.
  * src, dst     device int32 [n], n <= 2048.
  * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED (n > 2048: split the list where the
  * parts do not depend on one another's order), GDN_ERR_CUDA. n = 0 is a no-op. One launch, no
  * workspace.
  */
-gdn_status_t gdn_pages_copy(const void* src_pool, int64_t src_page_stride, int64_t src_layer_stride,
-                            int32_t src_pages, void* dst_pool, int64_t dst_page_stride,
-                            int64_t dst_layer_stride, int32_t dst_pages, int64_t page_bytes,
-                            int32_t layers, const int32_t* src, const int32_t* dst, int32_t n,
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t page_bytes;
+  int64_t src_page_stride, src_layer_stride;
+  int64_t dst_page_stride, dst_layer_stride;
+  int32_t layers;
+} gdn_page_pool_t;
+gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32_t src_pages,
+                            int32_t dst_pages, const int32_t* src, const int32_t* dst, int32_t n,
                             gdn_stream_t stream);
 
 /*
