@@ -3,7 +3,6 @@
 // A page holds one sequence's state (or its conv taps) of one layer. A copy moves whole pages,
 // so it is bound by HBM: 2 x page bytes for each entry. The lists, counts and plans are a few
 // ints per page and run in one CTA.
-#include <stdlib.h>
 #include "common.cuh"
 #include "launch.h"
 
@@ -48,6 +47,9 @@ template <int WARPS> __device__ __forceinline__ int block_scan(int v, int* warp_
 // is also a destination, a tile takes its columns of ALL entries, so no other CTA touches them
 // and the barrier is the only order needed; else a tile takes one entry's columns.
 
+// log2 of a tile's bytes: U 16-byte words of every thread
+__host__ __device__ constexpr int copy_tile_log(int U) { return U == 8 ? 16 : 14; }
+
 struct Table {
   int32_t* key;    // destination page, -1: empty
   int32_t* val;    // its last entry
@@ -74,47 +76,50 @@ pages_copy_kernel(const PagesCopy a, uint32_t slots) {
   int32_t* ms = sm + 2 * slots;       // [n] sources of the entries that count
   int32_t* md = ms + a.n;             // [n] their destinations
   __shared__ int sums[32], chained;
+  constexpr int K = kPagesMaxList / kCopyThreads;
+  int32_t es[K], ed[K];               // this thread's entries, i = k * kCopyThreads + threadIdx.x
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int i = k * kCopyThreads + threadIdx.x;
+    es[k] = i < a.n ? a.src[i] : -1;
+    ed[k] = i < a.n ? a.dst[i] : -1;
+  }
   if (threadIdx.x == 0) chained = 0;
   for (uint32_t s = threadIdx.x; s < slots; s += kCopyThreads) { tab.key[s] = -1; tab.val[s] = -1; }
   __syncthreads();
-  auto counts = [&](int i, int32_t& s, int32_t& d) {
-    s = a.src[i]; d = a.dst[i];
-    return s >= 0 && s < a.src_pages && d >= 0 && d < a.dst_pages;
-  };
-  for (int i = threadIdx.x; i < a.n; i += kCopyThreads) {
-    int32_t s, d;
-    if (!counts(i, s, d)) continue;
-    uint32_t h = slot_of(d, tab.mask);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (es[k] < 0 || es[k] >= a.src_pages || ed[k] < 0 || ed[k] >= a.dst_pages) { ed[k] = -1; continue; }
+    uint32_t h = slot_of(ed[k], tab.mask);
     while (true) {
-      const int32_t was = atomicCAS(&tab.key[h], -1, d);
-      if (was == -1 || was == d) break;
+      const int32_t was = atomicCAS(&tab.key[h], -1, ed[k]);
+      if (was == -1 || was == ed[k]) break;
       h = (h + 1) & tab.mask;
     }
-    atomicMax(&tab.val[h], i);
+    atomicMax(&tab.val[h], k * kCopyThreads + (int)threadIdx.x);
   }
   __syncthreads();
   // the entries that count, in the list's order: every CTA must number them alike
   int m = 0;
-  for (int i0 = 0; i0 < a.n; i0 += kCopyThreads) {
-    const int i = i0 + threadIdx.x;
-    int32_t s = -1, d = -1;
-    const bool on = i < a.n && counts(i, s, d) && find(tab, d) == i;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (k * kCopyThreads >= a.n) break;
+    const bool on = ed[k] >= 0 && find(tab, ed[k]) == k * kCopyThreads + (int)threadIdx.x;
     int total;
     const int at = m + block_scan<kCopyThreads / 32>(on, sums, total);
     if (on) {
-      ms[at] = s; md[at] = d;
-      if (s != d && find(tab, s) >= 0) chained = 1;
+      ms[at] = es[k]; md[at] = ed[k];
+      if (es[k] != ed[k] && find(tab, es[k]) >= 0) chained = 1;
     }
     m += total;
   }
   __syncthreads();
   if (m == 0) return;
 
-  constexpr int kLog = U == 8 ? 16 : U == 4 ? 15 : 14;             // bytes of a tile, a power of two
-  static_assert(kCopyThreads * U * 16 == 1 << kLog, "");
-  int64_t first = 0;                                               // this pool's first tile
+  constexpr int kLog = copy_tile_log(U);
+  uint32_t first = 0;                                              // this pool's first tile
   for (int k = 0; k < a.n_pools; ++k) {
-    const PagePool p = a.pool[k];
+    const PagePool& p = a.pool[k];
     // the tile: 2^lm entries x 2^lw bytes
     const bool clash = p.same && chained;
     int lw;
@@ -124,32 +129,34 @@ pages_copy_kernel(const PagesCopy a, uint32_t slots) {
       for (lw = 4; (1LL << lw) < p.page_bytes && lw < kLog;) ++lw;
     }
     const int lm = kLog - lw, lu = lw - 4;
-    const int64_t cols = (p.page_bytes + (1LL << lw) - 1) >> lw, groups = (m + (1LL << lm) - 1) >> lm;
-    const int64_t tiles = cols * groups * p.layers;
-    int64_t tile = (int64_t)blockIdx.x - first % gridDim.x;        // tiles of all pools in one round
-    if (tile < 0) tile += gridDim.x;
+    const uint32_t cols = (uint32_t)((p.page_bytes + (1LL << lw) - 1) >> lw), groups = ((uint32_t)(m - 1) >> lm) + 1;
+    const uint32_t tiles = cols * groups * p.layers;
+    uint32_t tile = (blockIdx.x + gridDim.x - first % gridDim.x) % gridDim.x;   // the pools' tiles in one round
     first += tiles;
     for (; tile < tiles; tile += gridDim.x) {
-      const int64_t rest = tile / groups, grp = tile - rest * groups;
-      const int64_t layer = rest / cols, col = (rest - layer * cols) << lw;
+      const uint32_t rest = tile / groups, grp = tile - rest * groups;
+      const uint32_t layer = rest / cols;
+      const int64_t col = (int64_t)(rest - layer * cols) << lw;
       const char* from = p.src + layer * p.src_layer + col;
       char* to = p.dst + layer * p.dst_layer + col;
+      const int64_t left = p.page_bytes - col;                     // bytes of a page from this column on
       uint4 v[U];
       int32_t e[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int idx = u * kCopyThreads + threadIdx.x;
         const int off = (idx & ((1 << lu) - 1)) << 4;
-        const int64_t at = (grp << lm) + (idx >> lu);
-        e[u] = at < m && col + off < p.page_bytes ? (int32_t)at : -1;
-        if (e[u] >= 0 && p.same && ms[at] == md[at]) e[u] = -1;
-        if (e[u] >= 0) v[u] = __ldcs(reinterpret_cast<const uint4*>(from + (int64_t)ms[at] * p.src_page + off));
+        e[u] = (int)(grp << lm) + (idx >> lu);
+        int32_t s = -1;
+        if (e[u] < m && off < left) s = ms[e[u]];
+        if (s < 0) e[u] = -1;
+        else v[u] = *reinterpret_cast<const uint4*>(from + s * p.src_page + off);
       }
       if (clash) __syncthreads();
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int off = ((u * kCopyThreads + threadIdx.x) & ((1 << lu) - 1)) << 4;
-        if (e[u] >= 0) __stcs(reinterpret_cast<uint4*>(to + (int64_t)md[e[u]] * p.dst_page + off), v[u]);
+        if (e[u] >= 0) __stcs(reinterpret_cast<uint4*>(to + md[e[u]] * p.dst_page + off), v[u]);
       }
     }
   }
@@ -241,6 +248,14 @@ pages_plan_kernel(int32_t* refs, int32_t n_pages, int32_t* table, int32_t n_tabl
   if (threadIdx.x == 0) *n_live = live_all;
 }
 
+// Tiles of a call at most, when every entry counts.
+int64_t copy_tiles(const PagesCopy& a, int log) {
+  int64_t tiles = 0;
+  for (int k = 0; k < a.n_pools; ++k)
+    tiles += (((a.pool[k].page_bytes + 15) >> 4) * a.n * a.pool[k].layers + (1 << (log - 4)) - 1) >> (log - 4);
+  return tiles;
+}
+
 template <int U>
 cudaError_t launch_copy(const PagesCopy& a, int sms, cudaStream_t st) {
   uint32_t slots = 32;
@@ -250,7 +265,8 @@ cudaError_t launch_copy(const PagesCopy& a, int sms, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(pages_copy_kernel<U>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  pages_copy_kernel<U><<<sms * 2, kCopyThreads, smem, st>>>(a, slots);
+  const int64_t tiles = copy_tiles(a, copy_tile_log(U)) + a.n_pools;
+  pages_copy_kernel<U><<<(unsigned)(tiles < sms * 2 ? tiles : sms * 2), kCopyThreads, smem, st>>>(a, slots);
   return cudaGetLastError();
 }
 
@@ -261,7 +277,10 @@ cudaError_t launch_pages_copy(const PagesCopy& a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  if (getenv("PG_U")) { int u = atoi(getenv("PG_U")); return u == 2 ? launch_copy<2>(a, sms, st) : u == 4 ? launch_copy<4>(a, sms, st) : launch_copy<8>(a, sms, st); }
+  // Large tiles keep more loads in flight and, where entries depend on one another, take longer
+  // runs of each page (200 chained pages of 2 MB: 163 us by 64 KB tiles, 201 by 32 KB, 307 by
+  // 16 KB); small ones spread a short copy over more SMs (one such page: 4.4 us by 16 KB, 5.7 by 64).
+  if (copy_tiles(a, copy_tile_log(8)) < 2 * sms) return launch_copy<2>(a, sms, st);
   return launch_copy<8>(a, sms, st);
 }
 
