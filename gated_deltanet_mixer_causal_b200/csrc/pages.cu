@@ -279,8 +279,10 @@ cudaError_t launch_pages_copy(const PagesCopy& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // Large tiles keep more loads in flight and, where entries depend on one another, take longer
   // runs of each page (200 chained pages of 2 MB: 163 us by 64 KB tiles, 201 by 32 KB, 307 by
-  // 16 KB); small ones spread a short copy over more SMs (one such page: 4.4 us by 16 KB, 5.7 by 64).
-  if (copy_tiles(a, copy_tile_log(8)) < 2 * sms) return launch_copy<2>(a, sms, st);
+  // 16 KB); small ones spread a short copy over more SMs (one such page: 4.4 us by 16 KB, 5.7 by
+  // 64). A tile must hold 16 bytes of every entry: 1,024 entries by 16 KB, 4,096 by 64 KB.
+  static_assert(kPagesMaxList << 4 <= 1 << copy_tile_log(8), "a tile holds the longest list");
+  if (a.n <= 256 && copy_tiles(a, copy_tile_log(8)) < 2 * sms) return launch_copy<2>(a, sms, st);
   return launch_copy<8>(a, sms, st);
 }
 
