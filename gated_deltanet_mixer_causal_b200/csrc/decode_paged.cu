@@ -9,39 +9,37 @@
 // and, when a gate is given, the block's output norm is applied where the head's whole output
 // lies in shared memory:  o_t <- o_t / sqrt(mean(o_t^2) + eps) * w * SiLU(z_t).
 //
-// One CTA owns one (sequence, key head): the conv channels of its q and k and of its G value
-// heads, so the in-place tap shift is race-free.
+// One cluster of C CTAs owns one (sequence, key head): the conv channels of its q and k and of
+// its G value heads, whose G D state rows are split evenly over the cluster. C is 1 where the
+// batch fills the GPU and grows as it shrinks.
+//
+// Bound by HBM: the state is read once and written once per stored token. What costs the
+// bandwidth is time in which an SM has no loads in flight (a page number is looked up, a conv
+// computed, before a row is used), so every lane runs a ring of asynchronous copies of the row
+// parts that it will itself consume, started before the conv: it needs no barrier, only the
+// lane's own wait.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "launch.h"
+
+namespace cg = cooperative_groups;
 
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kBlocks = 4;         // resident CTAs per SM
 constexpr int kWarps = kThreads / 32;
 constexpr float kEps = 1e-6f;
 constexpr int kMaxTok = 8;
 constexpr int kSeg = 16;           // state columns per lane
-constexpr int kRows = 2;           // state rows per lane and pass
+constexpr int kRows = 4;           // state rows per lane and pass
+constexpr int kAhead = 4;          // tokens whose channels are loaded together
+constexpr int kPass = 32 * kSeg * kRows;   // state elements of a warp's pass
 
-// Four consecutive state values, streamed (evict-first).
-template <typename S> struct Quad;
-template <> struct Quad<float> {
-  static __device__ __forceinline__ float4 load(const float* p) { return __ldcs(reinterpret_cast<const float4*>(p)); }
-  static __device__ __forceinline__ void store(float* p, float4 v) { __stcs(reinterpret_cast<float4*>(p), v); }
-};
-template <> struct Quad<bf16> {
-  static __device__ __forceinline__ float4 load(const bf16* p) {
-    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p));
-    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-  }
-  static __device__ __forceinline__ void store(bf16* p, float4 v) {
-    __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    __stcs(reinterpret_cast<uint2*>(p), make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b)));
-  }
-};
+// Stages of the ring: 8 KB a warp.
+template <typename S> constexpr int kStages = sizeof(S) == 4 ? 1 : 2;
 
 // z * sigmoid(z) for the activations' type: fp32 with the accurate exponential and division,
 // whose errors would otherwise show in fp32 results; bf16 with the fast ones.
@@ -49,32 +47,224 @@ template <typename T> __device__ __forceinline__ float silu_for(float z);
 template <> __device__ __forceinline__ float silu_for<bf16>(float z) { return silu(z); }
 template <> __device__ __forceinline__ float silu_for<float>(float z) { return z / (1.0f + expf(-z)); }
 
+// a * b + c. With fp32 activations every operation is rounded on its own, as the definition's
+// elementary operations are: states stored in bf16 then round the same way almost everywhere.
+template <typename T> __device__ __forceinline__ float mul_add(float a, float b, float c);
+template <> __device__ __forceinline__ float mul_add<bf16>(float a, float b, float c) { return fmaf(a, b, c); }
+template <> __device__ __forceinline__ float mul_add<float>(float a, float b, float c) { return __fadd_rn(__fmul_rn(a, b), c); }
+
+// Pairs of fp32 values: one instruction for two products or sums.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(f2 p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <typename T> __device__ __forceinline__ f2 mul_add2(f2 a, f2 b, f2 c);
+template <> __device__ __forceinline__ f2 mul_add2<bf16>(f2 a, f2 b, f2 c) { return fma2(a, b, c); }
+template <> __device__ __forceinline__ f2 mul_add2<float>(f2 a, f2 b, f2 c) { return add2(mul2(a, b), c); }
+
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Eight channels as they lie in memory.
+template <typename T> struct Raw8 {
+  uint4 u[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = make_uint4(0, 0, 0, 0);
+  }
+  // element i (a constant once unrolled)
+  __device__ __forceinline__ float get(int i) const {
+    const uint4 q = u[i * sizeof(T) / 16];
+    const int b = i % (16 / (int)sizeof(T));
+    if constexpr (sizeof(T) == 4) return __uint_as_float(b == 0 ? q.x : b == 1 ? q.y : b == 2 ? q.z : q.w);
+    const uint32_t w = b < 2 ? q.x : b < 4 ? q.y : b < 6 ? q.z : q.w;
+    return __uint_as_float(b & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+};
+
+// 16 bytes of a state row as pairs, and back (rounded to nearest even once for bf16).
+template <typename S> struct Chunk;
+template <> struct Chunk<float> {
+  static constexpr int kPairs = 2;
+  static __device__ __forceinline__ void get(uint4 u, f2* p) {
+    p[0] = pair(__uint_as_float(u.x), __uint_as_float(u.y));
+    p[1] = pair(__uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  static __device__ __forceinline__ uint4 put(const f2* p) {
+    const float2 a = unpair(p[0]), b = unpair(p[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+  }
+};
+template <> struct Chunk<bf16> {
+  static constexpr int kPairs = 4;
+  static __device__ __forceinline__ void get(uint4 u, f2* p) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint4 put(const f2* p) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpair(p[i]);
+      __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+      w[i] = *reinterpret_cast<uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// What the row loop needs of a token and value head. The state is carried as gamma times the
+// registers: a token that is neither stored nor near the ends of fp32 only multiplies gamma by its
+// alpha and adds (u / gamma) k, one instruction for two elements instead of two.
+struct __align__(16) Step {
+  float gamma;                     // alpha times the factor the registers carried before the token
+  float beta;
+  float inv;                       // 1 / gamma where the registers keep the factor, else 0: they
+                                   // become the state itself
+  float pad;
+};
+
+// Shared memory beside the ring, in floats: steps, q | k, v (then o), k.q, sums of o^2, 1 / rms.
+__host__ __device__ inline int64_t tile_floats(int n_tok, int64_t G, int d, int64_t rows) {
+  return (int64_t)n_tok * (2 * d + rows) + kMaxTok + 6 * G * n_tok;
+}
+
+// N sums (over the L lanes of a row) of each lane: every exchange leaves half of the sums with
+// each lane, so that log2(L) exchanges take 7 shuffles for 8 sums instead of 24. The sums end
+// in v[0 .. N / L - 1], lane seg holding those from seg * N / L on.
+template <int L, int N> __device__ __forceinline__ void scatter_sums(float* v, int seg) {
+  if constexpr (L > 1) {
+    const bool up = seg & (L / 2);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      v[i] = (up ? v[i + N / 2] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + N / 2], L / 2);
+    scatter_sums<L / 2, N / 2>(v, seg);
+  }
+}
+
+// Whether the registers may carry a factor: not with fp32 activations (see mul_add), and only where
+// the rows of a pass share one head's factor.
+template <typename T, int D> constexpr bool kCarry = sizeof(T) == 2 && kPass / D <= D;
+
 template <typename T, typename S, int D>
-__global__ void __launch_bounds__(kThreads, 2)
-decode_paged_kernel(const PagedDecode a) {
+__global__ void __launch_bounds__(kThreads, kBlocks)
+decode_paged_kernel(const PagedDecode a, int C) {
   constexpr int L = D / kSeg;              // lanes per state row
   constexpr int RPW = 32 / L;              // rows a warp covers at once
   constexpr int RPP = RPW * kRows;         // rows of a warp's pass
+  constexpr int CE = 16 / sizeof(S);       // elements of a 16-byte chunk
+  constexpr int CH = kSeg / CE;            // chunks of a lane's row part
+  constexpr int NST = kStages<S>;
   const int G = a.Hv / a.Hk, n_tok = a.n_tok;
   const int32_t Cc = 2 * a.Hk * D + a.Hv * D;
-  const int64_t b = blockIdx.x / a.Hk;
-  const int hk = blockIdx.x % a.Hk;
+  const int rank = blockIdx.x % C;
+  const int64_t b = blockIdx.x / C / a.Hk;
+  const int hk = blockIdx.x / C % a.Hk;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = G * D;
+  const int rows = G * D / C, row0 = rank * rows;      // this CTA's rows of the G D
 
-  int nv = n_tok;
-  if (a.n_valid) nv = min(max(a.n_valid[b], 0), n_tok);
-  if (nv == 0) return;                     // nothing of this sequence is read or written
+  // what does not depend on the page is asked for beside the page's number: the first channels'
+  // taps' weights and tokens
   const int32_t rp = a.read_pages[b];
+  const int nv = a.n_valid ? min(max(a.n_valid[b], 0), n_tok) : n_tok;
+  const T* x = static_cast<const T*>(a.x) + b * n_tok * a.x_stride;
+  const int n_local = 2 * D + rows;
+  int lc = threadIdx.x * 8;
+  auto channel = [&](int c) {              // of this CTA's local channel c, in the layer
+    return c < D ? hk * D + c : c < 2 * D ? a.Hk * D + hk * D + (c - D) : 2 * a.Hk * D + hk * G * D + row0 + (c - 2 * D);
+  };
+  Raw8<T> wr[4], xr[kAhead];
+  auto fetch_x = [&](int t0) {
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t)
+      if (t0 + t < n_tok) xr[t].load(x + (t0 + t) * a.x_stride + channel(lc));
+  };
+  auto fetch_w = [&]() {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) wr[j].load(static_cast<const T*>(a.conv_w) + (int64_t)channel(lc) * 4 + j * 8);
+  };
+  if (lc < n_local) { fetch_w(); fetch_x(0); }
+  if (nv == 0) return;                     // nothing of this sequence is computed, written or stored
   const bool fresh = rp < 0 || rp >= a.n_pages;
 
-  extern __shared__ float smem[];
-  float* qk = smem;                        // [n_tok][2 D] q | k
+  extern __shared__ __align__(16) char smem_raw[];
+  uint4* ring = reinterpret_cast<uint4*>(smem_raw) + warp * (NST * kRows * CH * 32) + lane;   // [stage][row][chunk][lane]
+  Step* steps = reinterpret_cast<Step*>(smem_raw + kWarps * NST * kPass * sizeof(S));         // [n_tok][G]
+  float* qk = reinterpret_cast<float*>(steps + n_tok * G);      // [n_tok][2 D]
   float* vo = qk + n_tok * 2 * D;          // [n_tok][rows] v, then o in its place
   float* kqs = vo + n_tok * rows;          // [kMaxTok] k_t.q_t
-  float2* ab = reinterpret_cast<float2*>(kqs + kMaxTok);        // [G][n_tok] (alpha, beta)
+  float* sqs = kqs + kMaxTok;              // [n_tok][G] sums of o^2 over this CTA's rows
+  float* rms = sqs + n_tok * G;            // [n_tok][G] 1 / rms of a head's o
   __shared__ int32_t wp[kMaxTok];          // page of the state after token t, -1: not stored
 
+  // 0. the first row parts are on their way before anything else is done
+  const int seg = lane % L;
+  const int64_t at0 = ((int64_t)hk * G * D + row0) * D + seg * CE;        // this lane's place in a page
+  const S* src = static_cast<const S*>(a.state_pool) + (fresh ? 0 : (int64_t)rp * a.state_stride) + at0;
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  auto fetch = [&](int pass, int stage) {
+    if (!fresh) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = pass * RPP + i * RPW + lane / L;
+        if (r < rows) {
+#pragma unroll
+          for (int j = 0; j < CH; ++j)
+            copy_async(ring_at + ((stage * kRows + i) * CH + j) * 512, src + (int64_t)r * D + j * CE * L);
+        }
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int st = 0; st < NST; ++st) fetch(warp + st * kWarps, st);
+
+  // 1. conv + SiLU over this CTA's channels, eight a thread; the window slides in registers. q and
+  //    k are laid out as the lanes of a row read them: quad i of a lane at 4 L i + 4 seg.
+  T* conv = static_cast<T*>(a.conv_pool);
+  Raw8<T> w0, w1, w2;
+  auto fetch_taps = [&]() {
+    w0.zero(); w1.zero(); w2.zero();
+    if (!fresh && lc < n_local) {
+      const T* cs = conv + (int64_t)rp * a.conv_stride + channel(lc);
+      w0.load(cs); w1.load(cs + Cc); w2.load(cs + 2 * Cc);
+    }
+  };
+  fetch_taps();
   if (threadIdx.x < kMaxTok) {
     const int t = threadIdx.x;
     int32_t p = -1;
@@ -85,45 +275,50 @@ decode_paged_kernel(const PagedDecode a) {
     }
     wp[t] = p;
   }
-  __syncthreads();
-
-  // 1. conv + SiLU over this CTA's channels; the window slides in registers
-  const T* x = static_cast<const T*>(a.x);
-  T* conv = static_cast<T*>(a.conv_pool);
-  for (int lc = threadIdx.x * 4; lc < 2 * D + rows; lc += kThreads * 4) {
-    int gc;
-    if (lc < D) gc = hk * D + lc;
-    else if (lc < 2 * D) gc = a.Hk * D + hk * D + (lc - D);
-    else gc = 2 * a.Hk * D + hk * G * D + (lc - 2 * D);
-    float w0[4], w1[4], w2[4], cur[4], wr[16];
-    VecIO<T, 16>::load(static_cast<const T*>(a.conv_w) + (int64_t)gc * 4, wr);
-    if (fresh) {
+  for (int i = threadIdx.x; i < G * nv; i += kThreads) {
+    const int64_t gi = (b * n_tok + i / G) * a.Hv + hk * G + i % G;
+    steps[i].gamma = expf(a.g[gi]);
+    steps[i].beta = a.beta[gi];
+  }
+  // the taps of q and k are read by the whole cluster before rank 0 writes them (all channels are
+  // in the loop's first round then); wp is visible behind the barrier
+  if (C > 1) cg::this_cluster().sync();
+  else __syncthreads();
+  while (lc < n_local) {
+    const int gc = channel(lc);
+    const bool keeps = rank == 0 || lc >= 2 * D;
+    const auto quad_at = [&](int c) {      // where four channels of q or k, or v, begin in shared memory
+      if (c >= 2 * D) return (int)(vo - qk) + c - 2 * D;
+      const int h = c < D ? 0 : D, cc = c - h;
+      return h + (cc / (CE * L) * CE + cc % CE) / 4 * (4 * L) + cc % (CE * L) / CE * 4;
+    };
+    const int at_a = quad_at(lc), at_b = quad_at(lc + 4), at_step = lc < 2 * D ? 2 * D : rows;
+    for (int t0 = 0; t0 < nv; t0 += kAhead) {
+      if (t0) fetch_x(t0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w0[i] = w1[i] = w2[i] = 0.f;
-    } else {
-      const T* cs = conv + (int64_t)rp * a.conv_stride + gc;
-      VecIO<T, 4>::load(cs, w0); VecIO<T, 4>::load(cs + Cc, w1); VecIO<T, 4>::load(cs + 2 * Cc, w2);
-    }
-    for (int t = 0; t < nv; ++t) {
-      VecIO<T, 4>::load(x + (b * n_tok + t) * a.x_stride + gc, cur);
-      float y[4];
+      for (int t = 0; t < kAhead; ++t) {
+        if (t0 + t >= nv) break;
+        float y[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float z = wr[i * 4] * w0[i];
-        z = fmaf(wr[i * 4 + 1], w1[i], z);
-        z = fmaf(wr[i * 4 + 2], w2[i], z);
-        z = fmaf(wr[i * 4 + 3], cur[i], z);
-        y[i] = silu_for<T>(z);
+        for (int i = 0; i < 8; ++i) {
+          float z = wr[i / 2].get(i % 2 * 4) * w0.get(i);
+          z = mul_add<T>(wr[i / 2].get(i % 2 * 4 + 1), w1.get(i), z);
+          z = mul_add<T>(wr[i / 2].get(i % 2 * 4 + 2), w2.get(i), z);
+          z = mul_add<T>(wr[i / 2].get(i % 2 * 4 + 3), xr[t].get(i), z);
+          y[i] = silu_for<T>(z);
+        }
+        float* dst = qk + (t0 + t) * at_step;
+        *reinterpret_cast<float4*>(dst + at_a) = make_float4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<float4*>(dst + at_b) = make_float4(y[4], y[5], y[6], y[7]);
+        if (keeps && wp[t0 + t] >= 0) {
+          T* cs = conv + (int64_t)wp[t0 + t] * a.conv_stride + gc;
+          w1.store(cs); w2.store(cs + Cc); xr[t].store(cs + 2 * Cc);
+        }
+        w0 = w1; w1 = w2; w2 = xr[t];
       }
-      float* dst = lc < 2 * D ? qk + t * 2 * D + lc : vo + t * rows + (lc - 2 * D);
-      *reinterpret_cast<float4*>(dst) = make_float4(y[0], y[1], y[2], y[3]);
-      if (wp[t] >= 0) {
-        T* cs = conv + (int64_t)wp[t] * a.conv_stride + gc;
-        VecIO<T, 4>::store(cs, w1); VecIO<T, 4>::store(cs + Cc, w2); VecIO<T, 4>::store(cs + 2 * Cc, cur);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { w0[i] = w1[i]; w1[i] = w2[i]; w2[i] = cur[i]; }
     }
+    lc += kThreads * 8;
+    if (lc < n_local) { fetch_w(); fetch_x(0); fetch_taps(); }
   }
   __syncthreads();
 
@@ -140,118 +335,233 @@ decode_paged_kernel(const PagedDecode a) {
       qq = fmaf(qv[j], qv[j], qq); kk = fmaf(kv[j], kv[j], kk); kq = fmaf(kv[j], qv[j], kq);
     }
     qq = warp_sum(qq); kk = warp_sum(kk); kq = warp_sum(kq);
-    const float iq = 1.0f / sqrtf(qq + kEps), ik = 1.0f / sqrtf(kk + kEps);
+    const float nq = sqrtf(qq + kEps), nk = sqrtf(kk + kEps);
     if (active) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) { yt[lane * VEC + j] = qv[j] * iq; yt[D + lane * VEC + j] = kv[j] * ik; }
+      for (int j = 0; j < VEC; ++j) { yt[lane * VEC + j] = qv[j] / nq; yt[D + lane * VEC + j] = kv[j] / nk; }
     }
-    if (lane == 0) kqs[t] = kq * iq * ik;
+    if (lane == 0) kqs[t] = kq / (nq * nk);
   }
-  for (int i = threadIdx.x; i < G * nv; i += kThreads) {
-    const int hh = i / nv, t = i % nv;
-    const int64_t gi = (b * n_tok + t) * a.Hv + hk * G + hh;
-    ab[hh * n_tok + t] = make_float2(expf(a.g[gi]), a.beta[gi]);
+  // the factor that the registers carry through the tokens of a head: it stays within 2^-40 and
+  // 2^40 (else, and where the token's state is stored, the registers become the state itself)
+  for (int hh = threadIdx.x; hh < G; hh += kThreads) {
+    constexpr float kLow = 0x1p-40f, kHigh = 0x1p40f;
+    float carried = 1.f;
+    for (int t = 0; t < nv; ++t) {
+      Step& st = steps[t * G + hh];
+      const float gamma = carried * st.gamma;
+      const float next = t + 1 < nv ? gamma * steps[(t + 1) * G + hh].gamma : 0.f;
+      const bool keep = kCarry<T, D> && wp[t] < 0 && gamma >= kLow && gamma <= kHigh && next >= kLow && next <= kHigh;
+      st.gamma = gamma;
+      st.inv = keep ? 1.0f / gamma : 0.f;
+      carried = keep ? gamma : 1.f;
+    }
   }
   __syncthreads();
 
   // 3. the state rows, each through every token
-  const int seg = lane % L;
-  const S* src = static_cast<const S*>(a.state_pool) + (fresh ? 0 : (int64_t)rp * a.state_stride);
-  const int64_t head0 = (int64_t)hk * G * D * D;        // this CTA's first element in a page
-  for (int p0 = warp * RPP; p0 < rows; p0 += kWarps * RPP) {
-    float s[kRows][kSeg];
-    int r[kRows];
+  S* pool = static_cast<S*>(a.state_pool) + at0;
+  int stage = 0;
+  for (int pass = warp; pass * RPP < rows; pass += kWarps) {
+    const int ra = pass * RPP + lane / L;            // this lane's first row; the others follow by RPW
+    f2 s[kRows][kSeg / 2];
+    copy_wait<NST - 1>();
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      r[i] = p0 + i * RPW + lane / L;
+    for (int i = 0; i < kRows; ++i)
 #pragma unroll
-      for (int j = 0; j < kSeg; j += 4) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!fresh && r[i] < rows) v = Quad<S>::load(src + head0 + (int64_t)r[i] * D + seg * 4 + j * L);
-        s[i][j] = v.x; s[i][j + 1] = v.y; s[i][j + 2] = v.z; s[i][j + 3] = v.w;
+      for (int j = 0; j < CH; ++j) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (!fresh && ra + i * RPW < rows) u = ring[((stage * kRows + i) * CH + j) * 32];
+        Chunk<S>::get(u, &s[i][j * Chunk<S>::kPairs]);
       }
-    }
-    for (int t = 0; t < nv; ++t) {
-      const float* qt = qk + t * 2 * D + seg * 4;
-      float kv[kSeg], sk[kRows], sq[kRows];
+    fetch(pass + NST * kWarps, stage);
+    stage = stage + 1 == NST ? 0 : stage + 1;
+    const float* qt = qk + seg * 4;
+    const Step* st = steps;
+    float* vt = vo;
+    for (int t = 0; t < nv; ++t, qt += 2 * D, st += G, vt += rows) {
+      // S k and S q of the lane's rows: first its own columns, then the row's lanes together
+      f2 acc[2 * kRows];
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) sk[i] = sq[i] = 0.f;
+      for (int i = 0; i < 2 * kRows; ++i) acc[i] = 0ull;
 #pragma unroll
-      for (int j = 0; j < kSeg; j += 4) {
-        const float4 q4 = *reinterpret_cast<const float4*>(qt + j * L);
-        const float4 k4 = *reinterpret_cast<const float4*>(qt + D + j * L);
-        kv[j] = k4.x; kv[j + 1] = k4.y; kv[j + 2] = k4.z; kv[j + 3] = k4.w;
+      for (int j = 0; j < kSeg / 4; ++j) {
+        const ulonglong2 q4 = *reinterpret_cast<const ulonglong2*>(qt + j * 4 * L);
+        const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(qt + D + j * 4 * L);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-          sk[i] = fmaf(s[i][j], k4.x, sk[i]); sk[i] = fmaf(s[i][j + 1], k4.y, sk[i]);
-          sk[i] = fmaf(s[i][j + 2], k4.z, sk[i]); sk[i] = fmaf(s[i][j + 3], k4.w, sk[i]);
-          sq[i] = fmaf(s[i][j], q4.x, sq[i]); sq[i] = fmaf(s[i][j + 1], q4.y, sq[i]);
-          sq[i] = fmaf(s[i][j + 2], q4.z, sq[i]); sq[i] = fmaf(s[i][j + 3], q4.w, sq[i]);
+          acc[i] = fma2(s[i][2 * j], k4.x, acc[i]);
+          acc[kRows + i] = fma2(s[i][2 * j], q4.x, acc[kRows + i]);
+          acc[i] = fma2(s[i][2 * j + 1], k4.y, acc[i]);
+          acc[kRows + i] = fma2(s[i][2 * j + 1], q4.y, acc[kRows + i]);
         }
       }
+      float sums[2 * kRows];
 #pragma unroll
-      for (int m = L / 2; m >= 1; m >>= 1)
+      for (int i = 0; i < 2 * kRows; ++i) {
+        const float2 f = unpair(acc[i]);
+        sums[i] = f.x + f.y;
+      }
+      scatter_sums<L, 2 * kRows>(sums, seg);
+      // The lower half of a row's lanes holds S k, the upper half S q, of NR rows each from row
+      // r0 on (one lane: both, of all rows). The former make u, the latter the output.
+      constexpr int H = L > 1 ? L / 2 : 1, NR = kRows / H;
+      const int r0 = L > 1 ? seg % H * NR : 0;
+      const bool has_k = L == 1 || seg < H, has_q = L == 1 || seg >= H;
+      float u[NR], gam[kRows], inv[kRows];
+      if constexpr (RPP <= D) {             // a pass lies in one head
+        const float4 p = *reinterpret_cast<const float4*>(st + (row0 + pass * RPP) / D);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) { gam[i] = p.x; inv[i] = p.z; }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const int r = ra + (r0 + i) * RPW;
+          u[i] = p.y * ((r < rows ? vt[r] : 0.f) - p.x * sums[i]);
+        }
+      } else {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-          sk[i] += __shfl_xor_sync(0xffffffffu, sk[i], m);
-          sq[i] += __shfl_xor_sync(0xffffffffu, sq[i], m);
+          const int r = ra + i * RPW;
+          gam[i] = r < rows ? st[(row0 + r) / D].gamma : 0.f;
+          inv[i] = 0.f;
         }
-      const int32_t to = wp[t];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const int r = ra + (r0 + i) * RPW, rr = r < rows ? r : 0;
+          u[i] = st[(row0 + rr) / D].beta * (vt[rr] - st[(row0 + rr) / D].gamma * sums[i]);
+        }
+      }
+      f2 uu[kRows];
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        const bool live = r[i] < rows;
-        const int rr = live ? r[i] : 0;
-        const float2 sc = ab[(rr / D) * n_tok + t];
-        const float u = sc.y * (vo[t * rows + rr] - sc.x * sk[i]);
+        const float ui = L > 1 ? __shfl_sync(0xffffffffu, u[i % NR], (lane & ~(L - 1)) + i / NR) : u[i % NR];
+        uu[i] = pair(ui, ui);
+      }
+      if constexpr (L > 1) {                // the upper half takes the u of its own rows
 #pragma unroll
-        for (int j = 0; j < kSeg; ++j) s[i][j] = fmaf(sc.x, s[i][j], u * kv[j]);
-        __syncwarp();                       // every lane of the row has read v before o replaces it
-        if (live && seg == 0) vo[t * rows + rr] = a.scale * fmaf(sc.x, sq[i], u * kqs[t]);
-        if (live && to >= 0) {
-          S* dst = static_cast<S*>(a.state_pool) + (int64_t)to * a.state_stride + head0 + (int64_t)rr * D + seg * 4;
+        for (int i = 0; i < NR; ++i) u[i] = __shfl_sync(0xffffffffu, u[i], (lane & ~(L - 1)) + seg % H);
+      }
+      __syncwarp();                         // v has been read where o is written
+      if (has_q) {
+        const float kq = kqs[t];
 #pragma unroll
-          for (int j = 0; j < kSeg; j += 4)
-            Quad<S>::store(dst + j * L, make_float4(s[i][j], s[i][j + 1], s[i][j + 2], s[i][j + 3]));
+        for (int i = 0; i < NR; ++i) {
+          const int r = ra + (r0 + i) * RPW;
+          if (r < rows) {
+            const float gm = RPP <= D ? gam[0] : st[(row0 + r) / D].gamma;
+            vt[r] = a.scale * fmaf(gm, sums[L > 1 ? i : kRows + i], u[i] * kq);
+          }
+        }
+      }
+      if (kCarry<T, D> && inv[0] != 0.f) {
+        const f2 iv = pair(inv[0], inv[0]);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) uu[i] = mul2(uu[i], iv);
+#pragma unroll
+        for (int j = 0; j < kSeg / 4; ++j) {
+          const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(qt + D + j * 4 * L);
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            s[i][2 * j] = fma2(uu[i], k4.x, s[i][2 * j]);
+            s[i][2 * j + 1] = fma2(uu[i], k4.y, s[i][2 * j + 1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kSeg / 4; ++j) {
+          const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(qt + D + j * 4 * L);
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            const f2 aa = pair(gam[i], gam[i]);
+            s[i][2 * j] = mul_add2<T>(aa, s[i][2 * j], mul2(uu[i], k4.x));
+            s[i][2 * j + 1] = mul_add2<T>(aa, s[i][2 * j + 1], mul2(uu[i], k4.y));
+          }
+        }
+        const int32_t to = wp[t];
+        if (to >= 0) {
+          S* dst = pool + (int64_t)to * a.state_stride + (int64_t)ra * D;
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)
+            if (ra + i * RPW < rows) {
+#pragma unroll
+              for (int j = 0; j < CH; ++j)
+                __stcs(reinterpret_cast<uint4*>(dst + i * RPW * D + j * CE * L), Chunk<S>::put(&s[i][j * Chunk<S>::kPairs]));
+            }
         }
       }
     }
   }
   __syncthreads();
 
-  // 4. outputs, normalised and gated when asked (a warp per token and head)
-  T* o = static_cast<T*>(a.o);
-  for (int e = warp; e < nv * G; e += kWarps) {
-    const int t = e / G, hh = e % G;
-    const float* row = vo + t * rows + hh * D;
-    const int64_t tok = b * n_tok + t;
-    T* dst = o + (tok * a.Hv + hk * G + hh) * D;
-    float rstd = 1.f;
-    if (a.z) {
+  // 4. outputs, normalised and gated when asked: sums of squares per token and head, over the
+  //    cluster where its CTAs share a head
+  if (a.z) {
+    for (int e = warp; e < nv * G; e += kWarps) {
+      const int t = e / G, hh = e % G;
+      const int lo = max(hh * D, row0) - row0, hi = min(hh * D + D, row0 + rows) - row0;
       float ss = 0.f;
-      for (int i = lane; i < D; i += 32) ss = fmaf(row[i], row[i], ss);
-      rstd = 1.0f / sqrtf(warp_sum(ss) / D + a.eps);
+      for (int i = lo + lane; i < hi; i += 32) ss = fmaf(vo[t * rows + i], vo[t * rows + i], ss);
+      ss = warp_sum(ss);
+      if (lane == 0) sqs[e] = ss;
     }
-    for (int i = lane; i < D; i += 32) {
-      float v = row[i];
-      if (a.z) {
-        const float z = to_f(static_cast<const T*>(a.z)[tok * a.z_stride + (hk * G + hh) * D + i]);
-        v = v * rstd * to_f(static_cast<const T*>(a.norm_w)[i]) * silu_for<T>(z);
+    if (C > 1) {
+      cg::cluster_group cl = cg::this_cluster();
+      cl.sync();
+      for (int e = threadIdx.x; e < nv * G; e += kThreads) {
+        float ss = 0.f;
+        for (int k = 0; k < C; ++k) ss += cl.map_shared_rank(sqs, k)[e];
+        rms[e] = 1.0f / sqrtf(ss / D + a.eps);
       }
-      dst[i] = from_f<T>(v);
+      cl.sync();                            // no CTA leaves while another reads its sums
+    } else {
+      __syncthreads();
+      for (int e = threadIdx.x; e < nv * G; e += kThreads) rms[e] = 1.0f / sqrtf(sqs[e] / D + a.eps);
+      __syncthreads();
     }
+  }
+  T* o = static_cast<T*>(a.o);
+  for (int e = threadIdx.x * 4; e < nv * rows; e += kThreads * 4) {
+    const int t = e / rows, i = e % rows, r = row0 + i;
+    const int64_t tok = b * n_tok + t;
+    float v[4];
+    VecIO<float, 4>::load(vo + e, v);
+    if (a.z) {
+      float z[4], w[4];
+      VecIO<T, 4>::load(static_cast<const T*>(a.z) + tok * a.z_stride + hk * G * D + r, z);
+      VecIO<T, 4>::load(static_cast<const T*>(a.norm_w) + r % D, w);
+      const float rstd = rms[t * G + r / D];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = v[k] * rstd * w[k] * silu_for<T>(z[k]);
+    }
+    VecIO<T, 4>::store(o + (tok * a.Hv + hk * G) * D + r, v);
   }
 }
 
 template <typename T, typename S, int D>
 cudaError_t launch_d(const PagedDecode& a, cudaStream_t st) {
-  const size_t smem = decode_paged_smem(a.n_tok, a.Hv / a.Hk, D);
-  if (smem > 40 * 1024) {   // beside the kernel's few static bytes
-    cudaError_t e = cudaFuncSetAttribute(decode_paged_kernel<T, S, D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  decode_paged_kernel<T, S, D><<<(unsigned)((int64_t)a.B * a.Hk), kThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  const int G = a.Hv / a.Hk;
+  // The cluster: CTAs until the GPU's 4 x 148 places are taken, two where a second wave would be
+  // half empty or less.
+  const int64_t ctas = (int64_t)a.B * a.Hk, places = kBlocks * 148;
+  const auto splits = [&](int c) { return G * D % (c * (kPass / D)) == 0 && 2 * D + G * D / c <= kThreads * 8; };
+  int C = 1;
+  while (C < 8 && ctas * C * 2 <= places && splits(C * 2)) C *= 2;
+  if (ctas > places && ctas * 2 <= places * 3 && splits(2)) C = 2;
+  const size_t smem = decode_paged_smem(a.n_tok, G, D) - (size_t)a.n_tok * (G * D - G * D / C) * sizeof(float);
+  cudaError_t e = cudaFuncSetAttribute(decode_paged_kernel<T, S, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.B * a.Hk * C));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C; attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, decode_paged_kernel<T, S, D>, a, C);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T, typename S>
@@ -267,8 +577,8 @@ cudaError_t launch_ts(const PagedDecode& a, int d, cudaStream_t st) {
 }  // namespace
 
 size_t decode_paged_smem(int n_tok, int64_t G, int d) {
-  // q | k, v (then o), k.q, (alpha, beta)
-  return sizeof(float) * (size_t)((int64_t)n_tok * (2 + G) * d + kMaxTok + 2 * G * n_tok);
+  return (size_t)kWarps * kStages<float> * kPass * sizeof(float) +
+         sizeof(float) * (size_t)tile_floats(n_tok, G, d, G * d);
 }
 
 cudaError_t launch_decode_paged(int dtype, int state_dtype, int d, const PagedDecode& a, cudaStream_t st) {
