@@ -52,7 +52,7 @@ SIGNATURES = {
     "gdn_decode_paged": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _P, _I64, ctypes.c_int, _I32, _P, _P,
                                         _P, _P, _P, _P, _I64, _P, _F32, _P, ctypes.c_int, _I32, _I32,
                                         _I32, _I32, _I32, _I32, _F32, _P]),
-    "gdn_pages_copy": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _P, _I32, _P]),
+    "gdn_pages_copy": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _P, _I32, _I32, _P]),
     "gdn_pages_take": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P]),
     "gdn_pages_ref": (ctypes.c_int, [_P, _I32, _P, _I32, _I32, _P]),
     "gdn_pages_plan": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _P, _P, _P]),
@@ -372,10 +372,6 @@ def gdn_decode_tokens(x: torch.Tensor, conv_w: torch.Tensor, conv_state: torch.T
 # cheap: one comparison per tensor where it is as expected, and the reason worked out only where
 # it is not.
 
-def _raw_stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
 def _device_of(t: torch.Tensor, name: str) -> torch.device:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -384,26 +380,32 @@ def _device_of(t: torch.Tensor, name: str) -> torch.device:
 
 def _want(t: torch.Tensor, name: str, shape, dtype, device):
     """t is a dense tensor of this shape (a tuple), type and CUDA device."""
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
         return
     _need(t, name, shape, dtype, device)
 
 
 def _want_view(t: torch.Tensor, name: str, shape, dtype, device):
     """The same without the demand that it is dense."""
-    if t.dtype is dtype and t.shape == shape and t.device == device:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device.index:
         return
     _need(t, name, shape, dtype, device, dense=False)
 
 
+_current_stream = torch._C._cuda_getCurrentRawStream      # torch.cuda.current_stream(d).cuda_stream
+_functions = {}
+
+
 def _call(device: torch.device, name: str, *args):
     """lib().<name>(*args, stream) with the tensors' device current, and its status checked."""
-    fn = getattr(lib(), name)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(lib(), name)
     if torch.cuda.current_device() == device.index:
-        status = fn(*args, _raw_stream(device))
+        status = fn(*args, _current_stream(device.index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, _raw_stream(device))
+            status = fn(*args, _current_stream(device.index))
     if status != GDN_OK:
         _check(status, name)
 
@@ -424,7 +426,9 @@ def _dense_from(t: torch.Tensor, name: str, dim: int, what: str) -> int:
 
 def _token_rows(t: torch.Tensor, name: str, lead: int) -> int:
     """The token stride of t, whose first ``lead`` (1 or 2) dimensions count tokens that follow
-    one another at one stride; the dimensions behind them must be dense."""
+    one another at one stride; the dimensions behind them must be dense. 0 stands for a dense t."""
+    if t.is_contiguous():
+        return 0
     inner = _dense_from(t, name, lead, "the dimensions behind the tokens")
     shape, strides = t.shape, t.stride()
     if lead == 1:
@@ -434,6 +438,14 @@ def _token_rows(t: torch.Tensor, name: str, lead: int) -> int:
     if shape[0] > 1 and strides[0] != strides[1] * shape[1]:
         raise ValueError(f"{name}: tokens must follow one another at one stride, got strides {strides}")
     return strides[1]
+
+
+def _page_stride(t: torch.Tensor, name: str) -> int:
+    """The stride in elements between the dense pages of pool t; 0 stands for a dense pool."""
+    if t.is_contiguous():
+        return 0
+    page = _dense_from(t, name, 1, "pages")
+    return page if t.shape[0] <= 1 else t.stride(0)
 
 
 def gdn_decode_paged(x: torch.Tensor, conv_w: torch.Tensor, conv_pool: torch.Tensor, state_pool: torch.Tensor,
@@ -479,10 +491,8 @@ def gdn_decode_paged(x: torch.Tensor, conv_w: torch.Tensor, conv_pool: torch.Ten
         o = torch.empty((B, n_tok, Hv, dv), dtype=dt, device=dev)
     else:
         _want(o, "o", (B, n_tok, Hv, dv), dt, dev)
-    taps = _dense_from(conv_pool, "conv_pool", 1, "pages")
-    page = _dense_from(state_pool, "state_pool", 1, "pages")
     _call(dev, "gdn_decode_paged", x.data_ptr(), _token_rows(x, "x", 2), conv_w.data_ptr(), conv_pool.data_ptr(),
-          taps if P <= 1 else conv_pool.stride(0), state_pool.data_ptr(), page if P <= 1 else state_pool.stride(0),
+          _page_stride(conv_pool, "conv_pool"), state_pool.data_ptr(), _page_stride(state_pool, "state_pool"),
           _dtype_code(state_pool), P, read_pages.data_ptr(), _addr(write_pages), _addr(n_valid), g.data_ptr(),
           beta.data_ptr(), _addr(z), z_stride, _addr(norm_w), eps, o.data_ptr(), _dtype_code(x), B, n_tok, Hk, Hv,
           dk, dv, scale)
@@ -492,51 +502,79 @@ def gdn_decode_paged(x: torch.Tensor, conv_w: torch.Tensor, conv_pool: torch.Ten
 def _pool_layout(t: torch.Tensor, name: str, page_dim: int):
     """(pages, layers, page bytes, page stride, layer stride) in bytes of a pool [P, page..]
     (page_dim 0) or [layers, P, page..] (page_dim 1)."""
-    if t.dim() < page_dim + 2:
-        raise ValueError(f"{name} has {t.dim()} dimensions, too few for page_dim = {page_dim}")
-    es, shape, strides = t.element_size(), t.shape, t.stride()
-    page = _dense_from(t, name, page_dim + 1, "pages") * es
+    shape = t.shape
+    if len(shape) < page_dim + 2:
+        raise ValueError(f"{name} has {len(shape)} dimensions, too few for page_dim = {page_dim}")
+    es, strides = t.element_size(), t.stride()
     pages, layers = shape[page_dim], shape[0] if page_dim else 1
+    if pages > 1 and t.is_contiguous():
+        page = strides[page_dim] * es
+    else:
+        page = _dense_from(t, name, page_dim + 1, "pages") * es
     return pages, layers, page, strides[page_dim] * es if pages > 1 else page, strides[0] * es if layers > 1 else 0
 
 
-def gdn_pages_copy(src_pool, src: torch.Tensor, dst: torch.Tensor, dst_pool=None, page_dim: int = 0) -> None:
-    """Page src[i] of ``src_pool`` to page dst[i] of ``dst_pool`` (default: the same pool) for
-    every entry of the int32 lists, as if all were read before any is written; the last entry of
-    a repeated destination counts, entries that are not pages are skipped. Pools are [P, page..],
-    or [layers, P, page..] with ``page_dim`` = 1 (every layer is copied); a list of up to four
-    pools with equal P is copied by one call."""
+def _describe(froms, tos, page_dim: int, device: torch.device):
+    """The pools of a copy as gdn_pages_copy takes them: (array, source pages, destination pages)."""
     if page_dim not in (0, 1):
         raise ValueError(f"page_dim must be 0 or 1, got {page_dim}")
-    froms = [src_pool] if isinstance(src_pool, torch.Tensor) else list(src_pool)
-    tos = froms if dst_pool is None else [dst_pool] if isinstance(dst_pool, torch.Tensor) else list(dst_pool)
     if not 1 <= len(froms) <= 4 or len(tos) != len(froms):
         raise ValueError(f"expected 1 to 4 pools and as many destinations, got {len(froms)} and {len(tos)}")
-    dev = _device_of(froms[0], "src_pool")
     desc = (_PagePool * len(froms))()
     sp = dp = None
     for d, a, b in zip(desc, froms, tos):
         pages, layers, size, stride, layer = _pool_layout(a, "src_pool", page_dim)
         d.src, d.page_bytes, d.src_page_stride, d.src_layer_stride, d.layers = a.data_ptr(), size, stride, layer, layers
+        bad = size <= 0 or (size | stride | layer | d.src) & 15
         to_pages = pages
         if b is not a:
             to_pages, to_layers, to_size, stride, layer = _pool_layout(b, "dst_pool", page_dim)
             if b.dtype != a.dtype or to_layers != layers or to_size != size:
                 raise ValueError("source and destination pools must agree in dtype, layers and page size")
+            bad |= (stride | layer | b.data_ptr()) & 15
         d.dst, d.dst_page_stride, d.dst_layer_stride = b.data_ptr(), stride, layer
-        if a.device != dev or b.device != dev or sp not in (None, pages) or dp not in (None, to_pages):
-            raise ValueError("all pools must be on one device and agree in their number of pages")
+        if bad:
+            raise ValueError("pages must begin at, and be, multiples of 16 bytes")
+        if a.device != device or b.device != device or sp not in (None, pages) or dp not in (None, to_pages):
+            raise ValueError("all pools must be on the lists' device and agree in their number of pages")
         sp, dp = pages, to_pages
-    n = src.numel()
+    return desc, sp, dp
+
+
+def _pool_list(pools):
+    return [pools] if isinstance(pools, torch.Tensor) else list(pools)
+
+
+def _describe_counted(refs: torch.Tensor, pools, page_dim: int):
+    """_describe for pools whose pages ``refs`` counts, before anything is changed."""
+    pools = _pool_list(pools)
+    desc, pages, _ = _describe(pools, pools, page_dim, _device_of(refs, "refs"))
+    if pages != refs.numel():
+        raise ValueError(f"the pools have {pages} pages, refs has {refs.numel()}")
+    return desc, pages
+
+
+def gdn_pages_copy(src_pool, src: torch.Tensor, dst: torch.Tensor, dst_pool=None, page_dim: int = 0,
+                   plain: bool = False) -> None:
+    """Page src[i] of ``src_pool`` to page dst[i] of ``dst_pool`` (default: the same pool) for
+    every entry of the int32 lists, as if all were read before any is written; the last entry of
+    a repeated destination counts, entries that are not pages are skipped. Pools are [P, page..],
+    or [layers, P, page..] with ``page_dim`` = 1 (every layer is copied); a list of up to four
+    pools with equal P is copied by one call. ``plain``: no destination is named twice or is
+    another entry's source (faster)."""
+    froms = _pool_list(src_pool)
+    n, dev = src.numel(), _device_of(src, "src")
     _want(src, "src", (n,), torch.int32, dev)
     _want(dst, "dst", (n,), torch.int32, dev)
-    _call(dev, "gdn_pages_copy", ctypes.addressof(desc), len(froms), sp, dp, src.data_ptr(), dst.data_ptr(), n)
+    desc, sp, dp = _describe(froms, froms if dst_pool is None else _pool_list(dst_pool), page_dim, dev)
+    _call(dev, "gdn_pages_copy", ctypes.addressof(desc), len(desc), sp, dp, src.data_ptr(), dst.data_ptr(), n,
+          int(bool(plain)))
 
 
 def gdn_pages_take(refs: torch.Tensor, n: Optional[int] = None, src: Optional[torch.Tensor] = None,
                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Take the lowest free pages (count 0 in ``refs`` [P] int32), whose counts become 1: ``n`` of
-    them, or one for each entry of ``src`` that is a page. Returns them (int32, -1: none)."""
+    them, or one for each entry of ``src`` that is a page in use. Returns them (int32, -1: none)."""
     if (n is None) == (src is None):
         raise ValueError("give either n or src")
     dev, P = _device_of(refs, "refs"), refs.numel()
@@ -565,24 +603,32 @@ def gdn_pages_fork(refs: torch.Tensor, src: torch.Tensor, pools, page_dim: int =
                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """A new page for each entry of ``src`` (see ``gdn_pages_take``), holding a copy of page
     src[i] in each pool of ``pools``. Returns the new pages."""
+    desc, P = _describe_counted(refs, pools, page_dim)
     out = gdn_pages_take(refs, src=src, out=out)
-    gdn_pages_copy(pools, src, out, page_dim=page_dim)
+    _call(refs.device, "gdn_pages_copy", ctypes.addressof(desc), len(desc), P, P, src.data_ptr(), out.data_ptr(),
+          src.numel(), 1)
     return out
 
 
-def gdn_pages_plan(refs: torch.Tensor, table: Optional[torch.Tensor] = None):
-    """The moves that bring the live pages (count > 0) to the front: (src, dst, map, n_live), the
-    lists padded with -1; refs and the page numbers in ``table`` (any shape) are rewritten."""
+def _plan(refs: torch.Tensor, table: Optional[torch.Tensor]):
+    """(src | dst | map | n_live in one tensor, P / 2)"""
     dev, P = _device_of(refs, "refs"), refs.numel()
     _want(refs, "refs", (P,), torch.int32, dev)
     if table is not None:
         _want(table, "table", table.shape, torch.int32, dev)
     half = P // 2
     lists = torch.empty((2 * half + P + 1,), dtype=torch.int32, device=dev)
-    src, dst, new_of, n_live = lists[:half], lists[half:2 * half], lists[2 * half:-1], lists[-1:]
+    at = lists.data_ptr()
     _call(dev, "gdn_pages_plan", refs.data_ptr(), P, _addr(table), 0 if table is None else table.numel(),
-          src.data_ptr(), dst.data_ptr(), new_of.data_ptr(), n_live.data_ptr())
-    return src, dst, new_of, n_live
+          at, at + 4 * half, at + 8 * half, at + 8 * half + 4 * P)
+    return lists, half
+
+
+def gdn_pages_plan(refs: torch.Tensor, table: Optional[torch.Tensor] = None):
+    """The moves that bring the live pages (count > 0) to the front: (src, dst, map, n_live), the
+    lists padded with -1; refs and the page numbers in ``table`` (any shape) are rewritten."""
+    lists, half = _plan(refs, table)
+    return lists[:half], lists[half:2 * half], lists[2 * half:-1], lists[-1:]
 
 
 _MAX_LIST = 2048     # entries of one gdn_pages_copy call
@@ -591,10 +637,13 @@ _MAX_LIST = 2048     # entries of one gdn_pages_copy call
 def gdn_pages_compact(refs: torch.Tensor, table: Optional[torch.Tensor], pools, page_dim: int = 0):
     """Bring the live pages to the front of every pool: ``refs`` and ``table`` are rewritten.
     Returns (map [P]: each live page's new place, -1 for free ones; n_live [1]), on the device."""
-    src, dst, new_of, n_live = gdn_pages_plan(refs, table)
-    for i in range(0, src.numel(), _MAX_LIST):
-        gdn_pages_copy(pools, src[i:i + _MAX_LIST], dst[i:i + _MAX_LIST], page_dim=page_dim)
-    return new_of, n_live
+    desc, P = _describe_counted(refs, pools, page_dim)
+    lists, half = _plan(refs, table)
+    at = lists.data_ptr()
+    for i in range(0, half, _MAX_LIST):
+        _call(refs.device, "gdn_pages_copy", ctypes.addressof(desc), len(desc), P, P, at + 4 * i, at + 4 * (half + i),
+              min(_MAX_LIST, half - i), 1)
+    return lists[2 * half:-1], lists[-1:]
 
 
 def gdn_norm_bwd_workspace_size(D: int) -> int:

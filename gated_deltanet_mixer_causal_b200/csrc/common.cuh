@@ -153,4 +153,17 @@ __device__ __forceinline__ void seq_bounds(const int32_t* cu, int32_t n, int64_t
   bos = a; eos = b;
 }
 
+// Asynchronous copies of 16 bytes, global to shared memory; a thread waits for its own groups.
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// A kernel launched by launch_overlapped (launch.h) may begin while the one before it in the
+// stream runs; it touches no global memory before this wait, which ends when that kernel and its
+// writes are complete. allow_next_grid lets such a successor begin early.
+__device__ __forceinline__ void wait_for_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 }  // namespace gdn

@@ -20,6 +20,8 @@
 // lane's own wait.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -33,6 +35,7 @@ constexpr int kBlocks = 4;         // resident CTAs per SM
 constexpr int kWarps = kThreads / 32;
 constexpr float kEps = 1e-6f;
 constexpr int kMaxTok = 8;
+constexpr int kMaxSmem = 224 * 1024;
 constexpr int kSeg = 16;           // state columns per lane
 constexpr int kRows = 4;           // state rows per lane and pass
 constexpr int kAhead = 4;          // tokens whose channels are loaded together
@@ -83,12 +86,6 @@ __device__ __forceinline__ f2 add2(f2 a, f2 b) {
 template <typename T> __device__ __forceinline__ f2 mul_add2(f2 a, f2 b, f2 c);
 template <> __device__ __forceinline__ f2 mul_add2<bf16>(f2 a, f2 b, f2 c) { return fma2(a, b, c); }
 template <> __device__ __forceinline__ f2 mul_add2<float>(f2 a, f2 b, f2 c) { return add2(mul2(a, b), c); }
-
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Eight channels as they lie in memory.
 template <typename T> struct Raw8 {
@@ -197,6 +194,8 @@ decode_paged_kernel(const PagedDecode a, int C) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = G * D / C, row0 = rank * rows;      // this CTA's rows of the G D
 
+  allow_next_grid();
+  wait_for_previous_grid();
   // what does not depend on the page is asked for beside the page's number: the first channels'
   // taps' weights and tokens
   const int32_t rp = a.read_pages[b];
@@ -548,18 +547,21 @@ cudaError_t launch_d(const PagedDecode& a, cudaStream_t st) {
   while (C < 8 && ctas * C * 2 <= places && splits(C * 2)) C *= 2;
   if (ctas > places && ctas * 2 <= places * 3 && splits(2)) C = 2;
   const size_t smem = decode_paged_smem(a.n_tok, G, D) - (size_t)a.n_tok * (G * D - G * D / C) * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(decode_paged_kernel<T, S, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> prepared{0};
+  cudaError_t e = raise_smem_limit(decode_paged_kernel<T, S, D>, kMaxSmem, prepared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.B * a.Hk * C));
+  cfg.gridDim = dim3((unsigned)(ctas * C));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C; attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C; attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = C > 1 ? 1 : 0;
+  cfg.numAttrs = C > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, decode_paged_kernel<T, S, D>, a, C);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

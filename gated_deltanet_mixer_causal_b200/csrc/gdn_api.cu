@@ -448,7 +448,7 @@ gdn_status_t gdn_decode_paged(const void* x, int64_t x_stride, const void* conv_
 
 gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32_t src_pages,
                             int32_t dst_pages, const int32_t* src, const int32_t* dst, int32_t n,
-                            gdn_stream_t stream) {
+                            int32_t plain, gdn_stream_t stream) {
   if (n < 0 || src_pages < 0 || dst_pages < 0) return fail(GDN_ERR_INVALID_ARG, "pages_copy: negative count");
   if (n_pools < 1 || n_pools > gdn::kPagesMaxPools || !pools)
     return fail(GDN_ERR_INVALID_ARG, "pages_copy: %d pools, expected 1 to %d", n_pools, gdn::kPagesMaxPools);
@@ -489,7 +489,8 @@ gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32
                            p.dst_page_stride, p.dst_layer_stride, p.layers, same};
   }
   if (a.n_pools == 0) return ok();
-  return cuda_status(gdn::launch_pages_copy(a, (cudaStream_t)stream), "pages_copy launch");
+  if (!gdn::pages_copy_fits(a)) return fail(GDN_ERR_UNSUPPORTED, "pages_copy: too much for one launch; split the list");
+  return cuda_status(gdn::launch_pages_copy(a, plain != 0, (cudaStream_t)stream), "pages_copy launch");
 }
 
 gdn_status_t gdn_pages_take(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n, int32_t* out,

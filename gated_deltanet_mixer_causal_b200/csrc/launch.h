@@ -3,12 +3,43 @@
 #pragma once
 
 #include <cuda_runtime.h>
+
+#include <atomic>
 #include <stddef.h>
 #include <stdint.h>
 
 #include "gdn.h"
 
 namespace gdn {
+
+// Raises a kernel's limit of dynamic shared memory on the current device, once for each device
+// (numbers below 64; others every time). `prepared` is the kernel's own.
+template <typename K>
+inline cudaError_t raise_smem_limit(K kernel, int bytes, std::atomic<uint64_t>& prepared) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (prepared.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) prepared.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+// Launches a kernel that begins with wait_for_previous_grid (common.cuh), so that its launch
+// overlaps the end of the kernel before it.
+template <typename... P, typename... A>
+inline cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                                     A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid; cfg.blockDim = block; cfg.dynamicSmemBytes = smem; cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr; cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 constexpr int kF32 = 0;   // GDN_F32
 constexpr int kBF16 = 1;  // GDN_BF16
@@ -99,7 +130,9 @@ struct PagesCopy {
   int32_t src_pages, dst_pages;
   const int32_t* src; const int32_t* dst; int32_t n;
 };
-cudaError_t launch_pages_copy(const PagesCopy& a, cudaStream_t stream);
+// plain: no destination is named twice and none is another entry's source
+bool pages_copy_fits(const PagesCopy& a);           // one launch can number its tiles
+cudaError_t launch_pages_copy(const PagesCopy& a, bool plain, cudaStream_t stream);
 cudaError_t launch_pages_take(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n, int32_t* out,
                               cudaStream_t stream);
 cudaError_t launch_pages_ref(int32_t* refs, int32_t n_pages, const int32_t* pages, int32_t n, int32_t delta,

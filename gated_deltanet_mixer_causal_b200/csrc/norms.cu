@@ -90,6 +90,8 @@ __global__ void __launch_bounds__(kGatedThreads, 4)
 gated_norm_kernel(const T* o, const T* __restrict__ z, int64_t z_stride, const T* __restrict__ w, float eps, T* y,
                   uint32_t rows, uint32_t H, uint32_t magic) {
   constexpr int VEC = 16 / sizeof(T), LANES = D / VEC, RPW = 32 / LANES, U = 4;
+  allow_next_grid();
+  wait_for_previous_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = lane % LANES * VEC;
   const uint32_t r0 = (blockIdx.x * kGatedWarps + warp) * (RPW * U) + lane / LANES;
@@ -127,6 +129,7 @@ gated_norm_bwd_kernel(const T* __restrict__ o, const T* __restrict__ z, int64_t 
                       float eps, const T* dy, T* dout, T* __restrict__ dz, int64_t dz_stride,
                       float* __restrict__ part, uint32_t rows, uint32_t H, uint32_t magic) {
   constexpr int VEC = 16 / sizeof(T), LANES = D / VEC, RPW = 32 / LANES, U = 2;
+  wait_for_previous_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = lane % LANES * VEC;
   float wf[VEC], dw[VEC];
@@ -178,6 +181,7 @@ gated_norm_bwd_kernel(const T* __restrict__ o, const T* __restrict__ z, int64_t 
     }
   }
   if (part == nullptr) return;
+  allow_next_grid();
   __shared__ float acc[kGatedWarps][D];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
@@ -198,6 +202,8 @@ gated_norm_bwd_kernel(const T* __restrict__ o, const T* __restrict__ z, int64_t 
 __global__ void __launch_bounds__(1024)
 norm_dw_kernel(const float* __restrict__ part, int n_part, int D, float* __restrict__ dw) {
   __shared__ float acc[32][33];
+  allow_next_grid();
+  wait_for_previous_grid();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
   if (c < D)
@@ -243,6 +249,8 @@ __global__ void __launch_bounds__(MAXT)
 add_norm_kernel(const T* __restrict__ x, const R* res, const T* __restrict__ w, float scale, float w_add, float eps,
                 R* h, T* __restrict__ n, int64_t rows, int D) {
   __shared__ float sm[2][64];
+  allow_next_grid();
+  wait_for_previous_grid();
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = row < rows;
   float v[NV][VEC], ss = 0.f;
@@ -289,6 +297,7 @@ add_norm_bwd_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* _
                     float scale, float w_add, float eps, R* dres, T* __restrict__ dx,
                     float* __restrict__ part, int64_t rows, int D) {
   __shared__ float sm[2][64];
+  wait_for_previous_grid();
   const float inv_d = 1.0f / D;
   float dw[NV][VEC];
   Raw<T, VEC> wv[NV], dr[NV];
@@ -362,6 +371,7 @@ add_norm_bwd_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* _
     fetch_dh(row + step);
   }
   if (part == nullptr) return;
+  allow_next_grid();
   // the rows of the CTA take their turns at one row of parts
   float* mine = part + (int64_t)blockIdx.x * D;
   for (int y = 0; y < blockDim.y; ++y) {
@@ -394,9 +404,9 @@ AddShape add_shape(int D, int vec, int nv) {
 template <typename T, typename R, int VEC, int NV, int MAXT>
 cudaError_t add_fwd(const AddNorm& a, cudaStream_t st) {
   const AddShape s = add_shape(a.D, VEC, NV);
-  add_norm_kernel<T, R, VEC, NV, MAXT><<<(unsigned)((a.rows + s.ty - 1) / s.ty), dim3(s.tx, s.ty), 0, st>>>(
-      (const T*)a.x, (const R*)a.res, (const T*)a.w, a.scale, a.w_add, a.eps, (R*)a.h, (T*)a.n, a.rows, a.D);
-  return cudaGetLastError();
+  return launch_overlapped(add_norm_kernel<T, R, VEC, NV, MAXT>, dim3((unsigned)((a.rows + s.ty - 1) / s.ty)),
+                           dim3(s.tx, s.ty), 0, st, (const T*)a.x, (const R*)a.res, (const T*)a.w, a.scale, a.w_add,
+                           a.eps, (R*)a.h, (T*)a.n, a.rows, a.D);
 }
 
 // MINB CTAs of the backward pass are resident on each of 148 SMs; no more are launched, so that
@@ -407,11 +417,11 @@ cudaError_t add_bwd(const AddNorm& a, cudaStream_t st) {
   const AddShape s = add_shape(a.D, VEC, NV);
   const int64_t groups = (a.rows + s.ty - 1) / s.ty;
   const int parts = (int)(groups < MINB * 148 ? groups : MINB * 148);
-  add_norm_bwd_kernel<T, R, VEC, NV, MAXT, MINB><<<parts, dim3(s.tx, s.ty), 0, st>>>(
-      (const R*)a.h, (const T*)a.w, (const T*)a.n, (const R*)a.res, a.scale, a.w_add, a.eps, (R*)a.dres, (T*)a.dx,
-      a.dw ? a.part : nullptr, a.rows, a.D);
-  if (a.dw) norm_dw_kernel<<<(a.D + 31) / 32, dim3(32, 32), 0, st>>>(a.part, parts, a.D, a.dw);
-  return cudaGetLastError();
+  const cudaError_t e = launch_overlapped(add_norm_bwd_kernel<T, R, VEC, NV, MAXT, MINB>, dim3(parts), dim3(s.tx, s.ty),
+                                          0, st, (const R*)a.h, (const T*)a.w, (const T*)a.n, (const R*)a.res, a.scale,
+                                          a.w_add, a.eps, (R*)a.dres, (T*)a.dx, a.dw ? a.part : nullptr, a.rows, a.D);
+  return e != cudaSuccess || !a.dw ? e : launch_overlapped(norm_dw_kernel, dim3((a.D + 31) / 32), dim3(32, 32), 0, st,
+                                                           a.part, parts, a.D, a.dw);
 }
 
 template <typename T, typename R>
@@ -443,19 +453,19 @@ cudaError_t gated_d(const GatedNorm& a, cudaStream_t st) {
   constexpr int RPW = 32 / (D / (16 / (int)sizeof(T)));
   if (!a.back) {
     const int64_t per = (int64_t)kGatedWarps * RPW * 4;
-    gated_norm_kernel<T, D><<<(unsigned)((a.rows + per - 1) / per), kGatedThreads, 0, st>>>(
-        (const T*)a.o, (const T*)a.z, a.z_stride, (const T*)a.w, a.eps, (T*)a.y, (uint32_t)a.rows, (uint32_t)a.H,
-        0xFFFFFFFFu / (uint32_t)a.H);
-    return cudaGetLastError();
+    return launch_overlapped(gated_norm_kernel<T, D>, dim3((unsigned)((a.rows + per - 1) / per)), dim3(kGatedThreads), 0,
+                             st, (const T*)a.o, (const T*)a.z, a.z_stride, (const T*)a.w, a.eps, (T*)a.y,
+                             (uint32_t)a.rows, (uint32_t)a.H, 0xFFFFFFFFu / (uint32_t)a.H);
   }
   const int64_t per = (int64_t)kGatedWarps * RPW * 2;
   const int64_t groups = (a.rows + per - 1) / per;
   const int parts = (int)(groups < kGatedBwdBlocks * 148 ? groups : kGatedBwdBlocks * 148);   // one wave
-  gated_norm_bwd_kernel<T, D><<<parts, kGatedThreads, 0, st>>>(
-      (const T*)a.o, (const T*)a.z, a.z_stride, (const T*)a.w, a.eps, (const T*)a.dy, (T*)a.dout, (T*)a.dz, a.dz_stride,
-      a.dw ? a.part : nullptr, (uint32_t)a.rows, (uint32_t)a.H, 0xFFFFFFFFu / (uint32_t)a.H);
-  if (a.dw) norm_dw_kernel<<<(D + 31) / 32, dim3(32, 32), 0, st>>>(a.part, parts, D, a.dw);
-  return cudaGetLastError();
+  const cudaError_t e = launch_overlapped(
+      gated_norm_bwd_kernel<T, D>, dim3(parts), dim3(kGatedThreads), 0, st, (const T*)a.o, (const T*)a.z, a.z_stride,
+      (const T*)a.w, a.eps, (const T*)a.dy, (T*)a.dout, (T*)a.dz, a.dz_stride, a.dw ? a.part : nullptr, (uint32_t)a.rows,
+      (uint32_t)a.H, 0xFFFFFFFFu / (uint32_t)a.H);
+  return e != cudaSuccess || !a.dw ? e : launch_overlapped(norm_dw_kernel, dim3((D + 31) / 32), dim3(32, 32), 0, st,
+                                                           a.part, parts, D, a.dw);
 }
 
 template <typename T>

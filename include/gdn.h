@@ -399,9 +399,12 @@ gdn_status_t gdn_decode_paged(const void* x, int64_t x_stride, const void* conv_
  *              either the same pool (equal pointers and strides, src_pages = dst_pages) or do not
  *              overlap, and no two of the destinations overlap.
  * src, dst     device int32 [n], n <= 2048.
- * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED (n > 2048: split the list where the
- * parts do not depend on one another's order), GDN_ERR_CUDA. n = 0 is a no-op. One launch, no
- * workspace.
+ * plain        0, or 1 where the caller knows that no destination is named twice and that none is
+ *              another entry's source (gdn_pages_plan's lists, gdn_pages_take's new pages), which
+ *              is faster. Pages that are, all the same, have no defined contents afterwards.
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED (n > 2048, or more than one launch can
+ * take: split the list where the parts do not depend on one another's order), GDN_ERR_CUDA. n = 0
+ * is a no-op. One launch, no workspace.
  */
 typedef struct {
   const void* src;
@@ -413,7 +416,7 @@ typedef struct {
 } gdn_page_pool_t;
 gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32_t src_pages,
                             int32_t dst_pages, const int32_t* src, const int32_t* dst, int32_t n,
-                            gdn_stream_t stream);
+                            int32_t plain, gdn_stream_t stream);
 
 /*
  * gdn_pages_take, gdn_pages_ref, gdn_pages_plan -- the counts of a pool's pages: refs, device
@@ -421,8 +424,8 @@ gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32
  *
  * gdn_pages_take: out[i] (device int32 [n], n <= 2048) receives the lowest free page not taken
  *   before it, whose count becomes 1, for i = 0, 1, ...; -1 once none is free. With src (device
- *   int32 [n]) an entry whose src[i] is not a page gets -1 and takes none: gdn_pages_copy(src,
- *   out) then completes a fork.
+ *   int32 [n]) an entry whose src[i] is not a page that is in use gets -1 and takes none:
+ *   gdn_pages_copy(src, out, plain) then completes a fork.
  * gdn_pages_ref: refs[pages[i]] += delta for every entry that is a page (a page listed twice
  *   counts twice); counts below 0 become 0. delta = 1 shares pages, -1 frees them.
  * gdn_pages_plan: the moves that bring the live pages to the front: with n_live of them, the

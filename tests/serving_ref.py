@@ -55,10 +55,10 @@ def copied(src_pool, dst_pool, src, dst, page_dim):
 
 
 def taken(refs, src):
-    refs, out = list(refs), []
+    refs, before, out = list(refs), list(refs), []
     for s in src:
         free = [p for p, r in enumerate(refs) if r <= 0]
-        ok = (s is None or 0 <= s < len(refs)) and bool(free)
+        ok = (s is None or (0 <= s < len(refs) and before[s] > 0)) and bool(free)
         out.append(free[0] if ok else -1)
         if ok:
             refs[free[0]] = 1

@@ -33,7 +33,7 @@ def case(dev, B, n, Hk, Hv, d, act, st, P, seed, wide=False, gate=False):
 
 
 def ints(v, dev):
-    return None if v is None else torch.tensor(v, dtype=torch.int32, device=dev)
+    return None if v is None else torch.tensor([int(i) for i in v] if isinstance(v, np.ndarray) else v, dtype=torch.int32, device=dev)
 
 
 def run_and_check(name, c, read, write, n_valid, dev, eps=1e-6, scale=1.0):
@@ -272,7 +272,7 @@ def test_pages_take_and_ref(cuda_device, P, n):
     got = gdn.gdn_pages_take(t, src=ints(src, cuda_device))
     if want is None:
         free = np.flatnonzero(refs <= 0)
-        ok = [0 <= s < P for s in src]
+        ok = [0 <= s < P and refs[s] > 0 for s in src]
         out = [int(free[sum(ok[:i])]) if ok[i] else -1 for i in range(n)]
         want = refs.copy()
         want[[p for p in out if p >= 0]] = 1
