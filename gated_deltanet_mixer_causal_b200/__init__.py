@@ -9,6 +9,11 @@ block boundaries on request), ``gdn_chunk_prefill_workspace_size``,
 ``gdn_chunk_prefill_noalloc``, ``gdn_decode_step`` and ``gdn_decode_tokens`` (fp32 or bf16
 states, taken from the state tensor); ``prefill_layer`` chains the conv and the chunked
 prefill over one packed batch without copies.
+
+For servers that keep states in pages of a pool: ``gdn_decode_paged`` reads and writes pages,
+``gdn_pages_copy`` / ``_fork`` / ``_compact`` move them, ``gdn_pages_take`` / ``_ref`` /
+``_plan`` keep their counts. Around the block: ``gdn_gated_norm`` (the norm and gate of the
+mixer's output) and ``gdn_add_norm`` (residual add and norm), each with its ``_bwd``.
 """
 from __future__ import annotations
 
@@ -48,11 +53,16 @@ def prefill_layer(x: torch.Tensor, conv_w: torch.Tensor, g: torch.Tensor, beta: 
                   final_state: Optional[torch.Tensor] = None,
                   conv_state_out: Optional[torch.Tensor] = None, scale: float = 1.0,
                   y: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
-                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+                  workspace: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                  norm_w: Optional[torch.Tensor] = None, eps: float = 1e-6) -> torch.Tensor:
     """The mixer core over one packed batch: conv + SiLU, then the chunked gated delta
     rule with q/k L2 norm. Returns o [T, Hv, d]; fills final_state / conv_state_out when
-    given."""
+    given. With the gate z [T, Hv, d] and norm_w [d], o is normalised and gated in place
+    (``gdn_gated_norm``), as ``gdn_decode_paged`` does for single tokens."""
+    if (z is None) != (norm_w is None):
+        raise ValueError("z and norm_w come together")
     y = gdn_conv1d_silu(x, conv_w, cu_seqlens, conv_state_in, conv_state_out, y)
     q, k, v = qkv_views(y, Hk, Hv, d)
-    return gdn_chunk_prefill(q, k, v, g, beta, cu_seqlens, initial_state, final_state, scale,
-                             True, o, workspace)
+    o = gdn_chunk_prefill(q, k, v, g, beta, cu_seqlens, initial_state, final_state, scale,
+                          True, o, workspace)
+    return o if z is None else gdn_gated_norm(o, z, norm_w, eps, y=o)

@@ -356,3 +356,23 @@ def test_serving_run(cuda_device):
         for a, b in zip(got, o[T:]):
             check("serving run", "o", max(frob_rel(R.f64(a[h]), b[h]) for h in range(Hv)), 2e-2)
     check("serving run", "state", max(frob_rel(last[h], S[0, h]) for h in range(Hv)), 2e-2)
+
+
+@pytest.mark.parametrize("act", [BF, FP])
+def test_prefill_layer_with_the_output_norm(cuda_device, act):
+    """A prefilled prompt's last token equals the same token decoded from a page, gate and norm
+    included, and the prefill's whole output is gdn_gated_norm's of the plain one."""
+    dev, Hk, Hv, d, T = cuda_device, 2, 4, 64, 40
+    c = case(dev, 1, T, Hk, Hv, d, act, FP, 2, seed=31, gate=True)
+    x, z, g, beta = (c[k].squeeze(0) for k in ("x", "z", "g", "beta"))
+    plain = gdn.prefill_layer(x, c["conv_w"], g, beta, Hk, Hv, d)
+    o = gdn.prefill_layer(x, c["conv_w"], g, beta, Hk, Hv, d, z=z, norm_w=c["norm_w"])
+    assert torch.equal(o, gdn.gdn_gated_norm(plain, z, c["norm_w"]))
+    conv, state = torch.zeros_like(c["conv"]), torch.zeros_like(c["state"])
+    gdn.prefill_layer(x[:-1], c["conv_w"], g[:-1], beta[:-1], Hk, Hv, d, final_state=state[1:], conv_state_out=conv[1:])
+    last = gdn.gdn_decode_paged(x[None, -1:], c["conv_w"], conv, state, ints([1], dev), g[None, -1:], beta[None, -1:], Hk,
+                                z=z[None, -1:], norm_w=c["norm_w"])
+    # both pass through T tokens of fp32 sums and one storage rounding; o is rounded before its norm
+    # in the prefill, behind it in the decode
+    tol = 3 * R.HALF[act] + 2 * (3 * d + 40) * R.U * 8 + (2.0 ** -18 if act == BF else 2e-6)
+    check(f"prefill norm {act}", "o", frob_rel(R.f64(last[0, 0]), R.f64(o[-1])), tol)
