@@ -164,12 +164,15 @@ __host__ __device__ inline int64_t tile_floats(int n_tok, int64_t G, int d, int6
 // each lane, so that log2(L) exchanges take 7 shuffles for 8 sums instead of 24. The sums end
 // in v[0 .. N / L - 1], lane seg holding those from seg * N / L on.
 template <int L, int N> __device__ __forceinline__ void scatter_sums(float* v, int seg) {
-  if constexpr (L > 1) {
+  if constexpr (L > 1 && N > 1) {
     const bool up = seg & (L / 2);
 #pragma unroll
     for (int i = 0; i < N / 2; ++i)
       v[i] = (up ? v[i + N / 2] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + N / 2], L / 2);
     scatter_sums<L / 2, N / 2>(v, seg);
+  } else if constexpr (L > 1) {             // one sum left, shared by L lanes
+#pragma unroll
+    for (int m = L / 2; m >= 1; m >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
   }
 }
 
@@ -404,9 +407,9 @@ decode_paged_kernel(const PagedDecode a, int C) {
       scatter_sums<L, 2 * kRows>(sums, seg);
       // The lower half of a row's lanes holds S k, the upper half S q, of NR rows each from row
       // r0 on (one lane: both, of all rows). The former make u, the latter the output.
-      constexpr int H = L > 1 ? L / 2 : 1, NR = kRows / H;
-      const int r0 = L > 1 ? seg % H * NR : 0;
-      const bool has_k = L == 1 || seg < H, has_q = L == 1 || seg >= H;
+      constexpr int H = L > 1 ? L / 2 : 1, NR = kRows > H ? kRows / H : 1;
+      const int r0 = L > 1 ? seg % H * kRows / H : 0;
+      const bool has_q = L == 1 || seg >= H;
       float u[NR], gam[kRows], inv[kRows];
       if constexpr (RPP <= D) {             // a pass lies in one head
         const float4 p = *reinterpret_cast<const float4*>(st + (row0 + pass * RPP) / D);
@@ -433,7 +436,7 @@ decode_paged_kernel(const PagedDecode a, int C) {
       f2 uu[kRows];
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        const float ui = L > 1 ? __shfl_sync(0xffffffffu, u[i % NR], (lane & ~(L - 1)) + i / NR) : u[i % NR];
+        const float ui = L > 1 ? __shfl_sync(0xffffffffu, u[i % NR], (lane & ~(L - 1)) + i * H / kRows) : u[i % NR];
         uu[i] = pair(ui, ui);
       }
       if constexpr (L > 1) {                // the upper half takes the u of its own rows
