@@ -9,9 +9,10 @@
 // and, when a gate is given, the block's output norm is applied where the head's whole output
 // lies in shared memory:  o_t <- o_t / sqrt(mean(o_t^2) + eps) * w * SiLU(z_t).
 //
-// One cluster of C CTAs owns one (sequence, key head): the conv channels of its q and k and of
-// its G value heads, whose G D state rows are split evenly over the cluster. C is 1 where the
-// batch fills the GPU and grows as it shrinks.
+// One cluster of C CTAs owns KH neighbouring key heads of a sequence: the conv channels of their q
+// and k and of their G value heads, whose G D state rows (one run of a page) are split evenly over
+// the cluster. C is 1 where the batch fills the GPU and grows as it shrinks; KH is 1 for heads of
+// 128 and grows for narrower ones, whose rows alone would not pay for a CTA's start.
 //
 // Bound by HBM: the state is read once and written once per stored token. What costs the
 // bandwidth is time in which an SM has no loads in flight (a page number is looked up, a conv
@@ -155,9 +156,10 @@ struct __align__(16) Step {
   float pad;
 };
 
-// Shared memory beside the ring, in floats: steps, q | k, v (then o), k.q, sums of o^2, 1 / rms.
-__host__ __device__ inline int64_t tile_floats(int n_tok, int64_t G, int d, int64_t rows) {
-  return (int64_t)n_tok * (2 * d + rows) + kMaxTok + 6 * G * n_tok;
+// Shared memory: the ring, then in floats steps, q | k, v (then o), k.q, sums of o^2, 1 / rms.
+int64_t smem_bytes(int n_tok, int64_t KH, int64_t G, int d, int64_t rows) {
+  return kWarps * kStages<float> * kPass * (int64_t)sizeof(float) +
+         (int64_t)sizeof(float) * n_tok * (KH * 2 * d + rows + KH + 6 * G);
 }
 
 // N sums (over the L lanes of a row) of each lane: every exchange leaves half of the sums with
@@ -182,18 +184,19 @@ template <typename T, int D> constexpr bool kCarry = sizeof(T) == 2 && kPass / D
 
 template <typename T, typename S, int D>
 __global__ void __launch_bounds__(kThreads, kBlocks)
-decode_paged_kernel(const PagedDecode a, int C) {
+decode_paged_kernel(const PagedDecode a, int C, int KH) {
   constexpr int L = D / kSeg;              // lanes per state row
   constexpr int RPW = 32 / L;              // rows a warp covers at once
   constexpr int RPP = RPW * kRows;         // rows of a warp's pass
   constexpr int CE = 16 / sizeof(S);       // elements of a 16-byte chunk
   constexpr int CH = kSeg / CE;            // chunks of a lane's row part
   constexpr int NST = kStages<S>;
-  const int G = a.Hv / a.Hk, n_tok = a.n_tok;
+  const int G1 = a.Hv / a.Hk, G = KH * G1, W = KH * D, n_tok = a.n_tok;
   const int32_t Cc = 2 * a.Hk * D + a.Hv * D;
   const int rank = blockIdx.x % C;
-  const int64_t b = blockIdx.x / C / a.Hk;
-  const int hk = blockIdx.x / C % a.Hk;
+  const int per_seq = a.Hk / KH;
+  const int64_t b = blockIdx.x / C / per_seq;
+  const int hk = blockIdx.x / C % per_seq * KH;        // the first key head
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = G * D / C, row0 = rank * rows;      // this CTA's rows of the G D
 
@@ -204,10 +207,10 @@ decode_paged_kernel(const PagedDecode a, int C) {
   const int32_t rp = a.read_pages[b];
   const int nv = a.n_valid ? min(max(a.n_valid[b], 0), n_tok) : n_tok;
   const T* x = static_cast<const T*>(a.x) + b * n_tok * a.x_stride;
-  const int n_local = 2 * D + rows;
+  const int n_local = 2 * W + rows;
   int lc = threadIdx.x * 8;
   auto channel = [&](int c) {              // of this CTA's local channel c, in the layer
-    return c < D ? hk * D + c : c < 2 * D ? a.Hk * D + hk * D + (c - D) : 2 * a.Hk * D + hk * G * D + row0 + (c - 2 * D);
+    return c < W ? hk * D + c : c < 2 * W ? a.Hk * D + hk * D + (c - W) : 2 * a.Hk * D + hk * G1 * D + row0 + (c - 2 * W);
   };
   Raw8<T> wr[4], xr[kAhead];
   auto fetch_x = [&](int t0) {
@@ -226,24 +229,32 @@ decode_paged_kernel(const PagedDecode a, int C) {
   extern __shared__ __align__(16) char smem_raw[];
   uint4* ring = reinterpret_cast<uint4*>(smem_raw) + warp * (NST * kRows * CH * 32) + lane;   // [stage][row][chunk][lane]
   Step* steps = reinterpret_cast<Step*>(smem_raw + kWarps * NST * kPass * sizeof(S));         // [n_tok][G]
-  float* qk = reinterpret_cast<float*>(steps + n_tok * G);      // [n_tok][2 D]
-  float* vo = qk + n_tok * 2 * D;          // [n_tok][rows] v, then o in its place
-  float* kqs = vo + n_tok * rows;          // [kMaxTok] k_t.q_t
-  float* sqs = kqs + kMaxTok;              // [n_tok][G] sums of o^2 over this CTA's rows
+  float* qk = reinterpret_cast<float*>(steps + n_tok * G);      // [n_tok][KH][2 D] q | k
+  float* vo = qk + n_tok * 2 * W;          // [n_tok][rows] v, then o in its place
+  float* kqs = vo + n_tok * rows;          // [n_tok][KH] k_t.q_t
+  float* sqs = kqs + n_tok * KH;           // [n_tok][G] sums of o^2 over this CTA's rows
   float* rms = sqs + n_tok * G;            // [n_tok][G] 1 / rms of a head's o
   __shared__ int32_t wp[kMaxTok];          // page of the state after token t, -1: not stored
 
   // 0. the first row parts are on their way before anything else is done
   const int seg = lane % L;
-  const int64_t at0 = ((int64_t)hk * G * D + row0) * D + seg * CE;        // this lane's place in a page
+  const int64_t at0 = ((int64_t)hk * G1 * D + row0) * D + seg * CE;        // this lane's place in a page
   const S* src = static_cast<const S*>(a.state_pool) + (fresh ? 0 : (int64_t)rp * a.state_stride) + at0;
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  // a pass lies in one key head: its key head, first row and the row behind that key head's last
+  const int krows = rows / KH, kpasses = (krows + RPP - 1) / RPP, passes = KH * kpasses;
+  struct Pass { int head, row, end; };
+  auto pass_of = [&](int pass) {
+    const int j = KH > 1 ? pass / kpasses : 0;
+    return Pass{j, j * krows + (pass - j * kpasses) * RPP, j * krows + krows};
+  };
   auto fetch = [&](int pass, int stage) {
-    if (!fresh) {
+    if (!fresh && pass < passes) {
+      const Pass w = pass_of(pass);
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        const int r = pass * RPP + i * RPW + lane / L;
-        if (r < rows) {
+        const int r = w.row + i * RPW + lane / L;
+        if (r < w.end) {
 #pragma unroll
           for (int j = 0; j < CH; ++j)
             copy_async(ring_at + ((stage * kRows + i) * CH + j) * 512, src + (int64_t)r * D + j * CE * L);
@@ -278,7 +289,7 @@ decode_paged_kernel(const PagedDecode a, int C) {
     wp[t] = p;
   }
   for (int i = threadIdx.x; i < G * nv; i += kThreads) {
-    const int64_t gi = (b * n_tok + i / G) * a.Hv + hk * G + i % G;
+    const int64_t gi = (b * n_tok + i / G) * a.Hv + hk * G1 + i % G;
     steps[i].gamma = expf(a.g[gi]);
     steps[i].beta = a.beta[gi];
   }
@@ -288,13 +299,13 @@ decode_paged_kernel(const PagedDecode a, int C) {
   else __syncthreads();
   while (lc < n_local) {
     const int gc = channel(lc);
-    const bool keeps = rank == 0 || lc >= 2 * D;
+    const bool keeps = rank == 0 || lc >= 2 * W;
     const auto quad_at = [&](int c) {      // where four channels of q or k, or v, begin in shared memory
-      if (c >= 2 * D) return (int)(vo - qk) + c - 2 * D;
-      const int h = c < D ? 0 : D, cc = c - h;
-      return h + (cc / (CE * L) * CE + cc % CE) / 4 * (4 * L) + cc % (CE * L) / CE * 4;
+      if (c >= 2 * W) return (int)(vo - qk) + c - 2 * W;
+      const int h = c < W ? 0 : D, cw = c < W ? c : c - W, cc = cw % D;
+      return cw / D * (2 * D) + h + (cc / (CE * L) * CE + cc % CE) / 4 * (4 * L) + cc % (CE * L) / CE * 4;
     };
-    const int at_a = quad_at(lc), at_b = quad_at(lc + 4), at_step = lc < 2 * D ? 2 * D : rows;
+    const int at_a = quad_at(lc), at_b = quad_at(lc + 4), at_step = lc < 2 * W ? 2 * W : rows;
     for (int t0 = 0; t0 < nv; t0 += kAhead) {
       if (t0) fetch_x(t0);
 #pragma unroll
@@ -324,10 +335,10 @@ decode_paged_kernel(const PagedDecode a, int C) {
   }
   __syncthreads();
 
-  // 2. q_t and k_t L2-normalised in place (a warp per token), k_t.q_t beside them
+  // 2. q_t and k_t L2-normalised in place (a warp per token and key head), k_t.q_t beside them
   constexpr int VEC = D >= 32 ? D / 32 : 1;
-  for (int t = warp; t < nv; t += kWarps) {
-    float* yt = qk + t * 2 * D;
+  for (int e = warp; e < nv * KH; e += kWarps) {        // qk and kqs lie by token, then key head
+    float* yt = qk + e * 2 * D;
     const bool active = lane * VEC < D;
     float qv[VEC], kv[VEC], qq = 0.f, kk = 0.f, kq = 0.f;
 #pragma unroll
@@ -342,7 +353,7 @@ decode_paged_kernel(const PagedDecode a, int C) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) { yt[lane * VEC + j] = qv[j] / nq; yt[D + lane * VEC + j] = kv[j] / nk; }
     }
-    if (lane == 0) kqs[t] = kq / (nq * nk);
+    if (lane == 0) kqs[e] = kq / (nq * nk);
   }
   // the factor that the registers carry through the tokens of a head: it stays within 2^-40 and
   // 2^40 (else, and where the token's state is stored, the registers become the state itself)
@@ -364,8 +375,9 @@ decode_paged_kernel(const PagedDecode a, int C) {
   // 3. the state rows, each through every token
   S* pool = static_cast<S*>(a.state_pool) + at0;
   int stage = 0;
-  for (int pass = warp; pass * RPP < rows; pass += kWarps) {
-    const int ra = pass * RPP + lane / L;            // this lane's first row; the others follow by RPW
+  for (int pass = warp; pass < passes; pass += kWarps) {
+    const Pass w = pass_of(pass);
+    const int ra = w.row + lane / L, end = w.end;    // this lane's first row; the others follow by RPW
     f2 s[kRows][kSeg / 2];
     copy_wait<NST - 1>();
 #pragma unroll
@@ -373,15 +385,15 @@ decode_paged_kernel(const PagedDecode a, int C) {
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
         uint4 u = make_uint4(0, 0, 0, 0);
-        if (!fresh && ra + i * RPW < rows) u = ring[((stage * kRows + i) * CH + j) * 32];
+        if (!fresh && ra + i * RPW < end) u = ring[((stage * kRows + i) * CH + j) * 32];
         Chunk<S>::get(u, &s[i][j * Chunk<S>::kPairs]);
       }
     fetch(pass + NST * kWarps, stage);
     stage = stage + 1 == NST ? 0 : stage + 1;
-    const float* qt = qk + seg * 4;
+    const float* qt = qk + w.head * 2 * D + seg * 4;
     const Step* st = steps;
     float* vt = vo;
-    for (int t = 0; t < nv; ++t, qt += 2 * D, st += G, vt += rows) {
+    for (int t = 0; t < nv; ++t, qt += 2 * W, st += G, vt += rows) {
       // S k and S q of the lane's rows: first its own columns, then the row's lanes together
       f2 acc[2 * kRows];
 #pragma unroll
@@ -412,24 +424,24 @@ decode_paged_kernel(const PagedDecode a, int C) {
       const bool has_q = L == 1 || seg >= H;
       float u[NR], gam[kRows], inv[kRows];
       if constexpr (RPP <= D) {             // a pass lies in one head
-        const float4 p = *reinterpret_cast<const float4*>(st + (row0 + pass * RPP) / D);
+        const float4 p = *reinterpret_cast<const float4*>(st + (row0 + w.row) / D);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) { gam[i] = p.x; inv[i] = p.z; }
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
           const int r = ra + (r0 + i) * RPW;
-          u[i] = p.y * ((r < rows ? vt[r] : 0.f) - p.x * sums[i]);
+          u[i] = p.y * ((r < end ? vt[r] : 0.f) - p.x * sums[i]);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
           const int r = ra + i * RPW;
-          gam[i] = r < rows ? st[(row0 + r) / D].gamma : 0.f;
+          gam[i] = r < end ? st[(row0 + r) / D].gamma : 0.f;
           inv[i] = 0.f;
         }
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-          const int r = ra + (r0 + i) * RPW, rr = r < rows ? r : 0;
+          const int r = ra + (r0 + i) * RPW, rr = r < end ? r : 0;
           u[i] = st[(row0 + rr) / D].beta * (vt[rr] - st[(row0 + rr) / D].gamma * sums[i]);
         }
       }
@@ -445,11 +457,11 @@ decode_paged_kernel(const PagedDecode a, int C) {
       }
       __syncwarp();                         // v has been read where o is written
       if (has_q) {
-        const float kq = kqs[t];
+        const float kq = kqs[t * KH + w.head];
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
           const int r = ra + (r0 + i) * RPW;
-          if (r < rows) {
+          if (r < end) {
             const float gm = RPP <= D ? gam[0] : st[(row0 + r) / D].gamma;
             vt[r] = a.scale * fmaf(gm, sums[L > 1 ? i : kRows + i], u[i] * kq);
           }
@@ -484,7 +496,7 @@ decode_paged_kernel(const PagedDecode a, int C) {
           S* dst = pool + (int64_t)to * a.state_stride + (int64_t)ra * D;
 #pragma unroll
           for (int i = 0; i < kRows; ++i)
-            if (ra + i * RPW < rows) {
+            if (ra + i * RPW < end) {
 #pragma unroll
               for (int j = 0; j < CH; ++j)
                 __stcs(reinterpret_cast<uint4*>(dst + i * RPW * D + j * CE * L), Chunk<S>::put(&s[i][j * Chunk<S>::kPairs]));
@@ -529,27 +541,37 @@ decode_paged_kernel(const PagedDecode a, int C) {
     VecIO<float, 4>::load(vo + e, v);
     if (a.z) {
       float z[4], w[4];
-      VecIO<T, 4>::load(static_cast<const T*>(a.z) + tok * a.z_stride + hk * G * D + r, z);
+      VecIO<T, 4>::load(static_cast<const T*>(a.z) + tok * a.z_stride + hk * G1 * D + r, z);
       VecIO<T, 4>::load(static_cast<const T*>(a.norm_w) + r % D, w);
       const float rstd = rms[t * G + r / D];
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = v[k] * rstd * w[k] * silu_for<T>(z[k]);
     }
-    VecIO<T, 4>::store(o + (tok * a.Hv + hk * G) * D + r, v);
+    VecIO<T, 4>::store(o + (tok * a.Hv + hk * G1) * D + r, v);
   }
 }
 
 template <typename T, typename S, int D>
 cudaError_t launch_d(const PagedDecode& a, cudaStream_t st) {
-  const int G = a.Hv / a.Hk;
-  // The cluster: CTAs until the GPU's 4 x 148 places are taken, two where a second wave would be
-  // half empty or less.
-  const int64_t ctas = (int64_t)a.B * a.Hk, places = kBlocks * 148;
+  const int G = a.Hv / a.Hk, places = kBlocks * 148;
+  // Key heads a CTA: for heads below 128, neighbours up to 768 rows in all, while the CTAs still
+  // fill the GPU's places and four of them an SM's shared memory. (256 sequences of 16 / 48 heads,
+  // heads of 64, fp32 states: 82.8 -> 78.5 us; heads of 32,
+  // bf16 states: 34.3 -> 20.4 us.)
+  int KH = 1;
+  while (D < 128 && a.Hk % (KH * 2) == 0 && KH * 2 * G * D <= 768 && (int64_t)a.B * a.Hk / (KH * 2) >= places &&
+         smem_bytes(a.n_tok, KH * 2, KH * 2 * G, D, KH * 2 * G * D) <= 56 * 1024)
+    KH *= 2;
+  // The cluster: CTAs until the GPU's places are taken, two where a second wave would be half
+  // empty or less.
+  const int64_t ctas = (int64_t)a.B * (a.Hk / KH);
   const auto splits = [&](int c) { return G * D % (c * (kPass / D)) == 0 && 2 * D + G * D / c <= kThreads * 8; };
   int C = 1;
-  while (C < 8 && ctas * C * 2 <= places && splits(C * 2)) C *= 2;
-  if (ctas > places && ctas * 2 <= places * 3 && splits(2)) C = 2;
-  const size_t smem = decode_paged_smem(a.n_tok, G, D) - (size_t)a.n_tok * (G * D - G * D / C) * sizeof(float);
+  if (KH == 1) {
+    while (C < 8 && ctas * C * 2 <= places && splits(C * 2)) C *= 2;
+    if (ctas > places && ctas * 2 <= places * 3 && splits(2)) C = 2;
+  }
+  const size_t smem = (size_t)smem_bytes(a.n_tok, KH, KH * G, D, KH * G * D / C);
   static std::atomic<uint64_t> prepared{0};
   cudaError_t e = raise_smem_limit(decode_paged_kernel<T, S, D>, kMaxSmem, prepared);
   if (e != cudaSuccess) return e;
@@ -565,7 +587,7 @@ cudaError_t launch_d(const PagedDecode& a, cudaStream_t st) {
   attr[1].val.clusterDim.x = C; attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, decode_paged_kernel<T, S, D>, a, C);
+  e = cudaLaunchKernelEx(&cfg, decode_paged_kernel<T, S, D>, a, C, KH);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -581,10 +603,7 @@ cudaError_t launch_ts(const PagedDecode& a, int d, cudaStream_t st) {
 
 }  // namespace
 
-size_t decode_paged_smem(int n_tok, int64_t G, int d) {
-  return (size_t)kWarps * kStages<float> * kPass * sizeof(float) +
-         sizeof(float) * (size_t)tile_floats(n_tok, G, d, G * d);
-}
+size_t decode_paged_smem(int n_tok, int64_t G, int d) { return (size_t)smem_bytes(n_tok, 1, G, d, G * d); }
 
 cudaError_t launch_decode_paged(int dtype, int state_dtype, int d, const PagedDecode& a, cudaStream_t st) {
   if (dtype == kF32)

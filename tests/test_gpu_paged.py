@@ -145,6 +145,22 @@ def test_paged_equals_the_dense_decode(cuda_device):
     assert frob_rel(R.f64(o), R.f64(ref)) <= 2 * R.HALF[BF]
 
 
+@pytest.mark.parametrize("B,Hk,Hv,d,n,st", [(150, 16, 32, 64, 2, FP), (160, 16, 48, 32, 3, BF), (620, 8, 8, 16, 1, FP),
+                                              (300, 16, 16, 16, 5, BF)])
+def test_paged_equals_the_dense_decode_for_many_narrow_heads(cuda_device, B, Hk, Hv, d, n, st):
+    """Batches that fill the GPU with heads below 128, where a CTA takes several key heads."""
+    c = case(cuda_device, B, n, Hk, Hv, d, BF, st, B, seed=d + n)
+    conv, state = c["conv"].clone(), c["state"].clone()
+    o = gdn.gdn_decode_paged(c["x"], c["conv_w"], c["conv"], c["state"], ints(list(range(B)), cuda_device), c["g"],
+                             c["beta"], Hk)
+    ref = gdn.gdn_decode_tokens(c["x"].contiguous(), c["conv_w"], conv, c["g"], c["beta"], state, Hk)
+    assert torch.equal(conv, c["conv"])
+    # either is off by n (3 d + 40) roundings at most, and the fast SiLU, before it is stored
+    tol = 2 * (n * (3 * d + 40) * R.U + 4 * 2.0 ** -20)
+    assert frob_rel(R.f64(c["state"]), R.f64(state)) <= tol + 2 * (R.HALF[BF] if st == BF else 0)
+    assert frob_rel(R.f64(o), R.f64(ref)) <= tol + 2 * R.HALF[BF]
+
+
 def test_paged_interleaved_pools(cuda_device):
     """Taps and state of a page side by side in one buffer, at page strides that are not dense."""
     c = case(cuda_device, 3, 2, 1, 2, 16, FP, FP, 5, seed=8)
