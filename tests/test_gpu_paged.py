@@ -80,7 +80,7 @@ BF, FP = torch.bfloat16, torch.float32
 @pytest.mark.parametrize("act", [BF, FP])
 @pytest.mark.parametrize("st", [BF, FP])
 @pytest.mark.parametrize("Hk,Hv,d,n", [(2, 6, 128, 1), (2, 4, 128, 4), (1, 1, 64, 3), (2, 10, 32, 8), (3, 3, 16, 5),
-                                       (1, 7, 16, 2)])
+                                       (1, 7, 16, 2), (1, 3, 128, 8), (2, 2, 128, 5), (4, 12, 128, 2), (1, 9, 128, 3)])
 def test_paged_types_and_heads(cuda_device, act, st, Hk, Hv, d, n):
     B, P = 5, 24
     c = case(cuda_device, B, n, Hk, Hv, d, act, st, P, seed=Hv * d + n, wide=True, gate=n % 2 == 0)
@@ -104,17 +104,18 @@ def test_paged_nothing_valid_touches_nothing(cuda_device):
     run_and_check("paged none valid", c, [0, 1, 2], None, [0, -3, 0], cuda_device)
 
 
-def test_paged_nan_in_unused_places(cuda_device):
+@pytest.mark.parametrize("act,d", [(FP, 64), (BF, 128)])
+def test_paged_nan_in_unused_places(cuda_device, act, d):
     """NaN in tokens behind n_valid, in pages nobody reads and in the page of a fresh sequence's
     neighbour reaches no output."""
-    c = case(cuda_device, 3, 3, 2, 4, 64, FP, FP, 6, seed=5, gate=True)
+    c = case(cuda_device, 3, 3, 2, 4, d, act, FP, 6, seed=5, gate=True)
     for key in ("x", "g", "beta", "z"):
         c[key][0, 1:] = float("nan")
         c[key][2] = float("nan")
     c["state"][3:] = float("nan")
     c["conv"][3:] = float("nan")
     read, valid, write = [0, -1, 1], [1, 3, 0], [[4, 4, 4], [2, -1, 5], [1, 1, 1]]
-    o = torch.zeros(3, 3, 4, 64, device=cuda_device)
+    o = torch.zeros(3, 3, 4, d, dtype=act, device=cuda_device)
     gdn.gdn_decode_paged(c["x"], c["conv_w"], c["conv"], c["state"], ints(read, cuda_device), c["g"], c["beta"], 2,
                          write_pages=ints(write, cuda_device), n_valid=ints(valid, cuda_device), z=c["z"],
                          norm_w=c["norm_w"], o=o)
@@ -122,15 +123,18 @@ def test_paged_nan_in_unused_places(cuda_device):
     assert torch.isfinite(c["conv"][[0, 1, 2, 4, 5]]).all() and torch.isnan(c["state"][3]).all()
 
 
-def test_paged_extremes_of_the_gates(cuda_device):
-    """alpha = 0 (g = -inf) drops the state, beta = 0 writes nothing, both beside ordinary heads;
-    a zero k or q stays zero under the norm's eps."""
-    c = case(cuda_device, 2, 3, 1, 4, 32, FP, FP, 4, seed=6)
+@pytest.mark.parametrize("act,d,n", [(FP, 32, 3), (BF, 128, 3), (BF, 128, 8), (BF, 64, 4)])
+def test_paged_extremes_of_the_gates(cuda_device, act, d, n):
+    """alpha = 0 (g = -inf) drops the state, decays of e^-25 a token pass the range that a factor is
+    carried in, beta = 0 writes nothing, all beside ordinary heads; a zero k or q stays zero under
+    the norm's eps."""
+    c = case(cuda_device, 3, n, 1, 4, d, act, FP, 4, seed=6)
     c["g"][0, 1] = float("-inf")
+    c["g"][2, :, :2] = -25.0
     c["beta"][1, :, 2] = 0
-    c["x"][1, :, :64] = 0
-    c["conv"][1, :, :64] = 0
-    run_and_check("paged gates", c, [0, 1], None, None, cuda_device)
+    c["x"][1, :, :2 * d] = 0
+    c["conv"][1, :, :2 * d] = 0
+    run_and_check(f"paged gates {act} {d} {n}", c, [0, 1, 2], None, None, cuda_device)
 
 
 def test_paged_equals_the_dense_decode(cuda_device):
