@@ -11,6 +11,12 @@
 // All four are bound by HBM: every element is read once and written once, the rows stay in
 // registers between their reduction and their use. Weight gradients are summed in fp32 in a
 // fixed order: registers of a thread over its rows, the threads of a CTA, then the CTAs.
+//
+// Measured, share of the bytes at the copy rate, bf16: gated 65,536 x 48 x 128 344 us (107 %:
+// two reads for a write), its backward 8,192 x 48 x 128 85 us (90 %; the second launch that adds
+// up dw and the fp32 instructions of two sigmoid factors an element take the rest); add norm
+// backward 16,384 x 4,096 with an fp32 residual 172 us (95 %). A decode batch of 64 tokens takes
+// 2.8 and 2.4 us, of which a launch is about 2.
 #include "common.cuh"
 #include "launch.h"
 

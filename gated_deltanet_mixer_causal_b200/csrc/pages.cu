@@ -2,7 +2,12 @@
 //
 // A page holds one sequence's state (or its conv taps) of one layer. A copy moves whole pages,
 // so it is bound by HBM: 2 x page bytes for each entry. The lists, counts and plans are a few
-// ints per page and run in one CTA.
+// ints per page and run in one CTA (3 to 4 us for 256 pages).
+//
+// Measured, share of the bytes at the copy rate: 200 pages of 2 MB 129 us (100 %); 256 pages of
+// 3.2 MB compacted, plan included, 69 us (90 %); one page into 8 new ones in 4 layers, with the
+// taking of the pages, 25 us (70 %; writes alone are 17 us); 64 beams of 1.1 MB in 4 layers
+// reordered in place 96 us (72 %: short runs of every page in turn, see below).
 #include <atomic>
 
 #include "common.cuh"
