@@ -525,7 +525,7 @@ def _describe(froms, tos, page_dim: int, device: torch.device):
     for d, a, b in zip(desc, froms, tos):
         pages, layers, size, stride, layer = _pool_layout(a, "src_pool", page_dim)
         d.src, d.page_bytes, d.src_page_stride, d.src_layer_stride, d.layers = a.data_ptr(), size, stride, layer, layers
-        bad = size <= 0 or (size | stride | layer | d.src) & 15
+        bad = size <= 0 or (size | stride | layer | a.data_ptr()) & 15
         to_pages = pages
         if b is not a:
             to_pages, to_layers, to_size, stride, layer = _pool_layout(b, "dst_pool", page_dim)
