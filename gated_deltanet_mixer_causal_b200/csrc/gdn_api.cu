@@ -489,7 +489,7 @@ gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32
                            p.dst_page_stride, p.dst_layer_stride, p.layers, same};
   }
   if (a.n_pools == 0) return ok();
-  if (!gdn::pages_copy_fits(a)) return fail(GDN_ERR_UNSUPPORTED, "pages_copy: too much for one launch; split the list");
+  if (!gdn::pages_copy_fits(a, plain != 0)) return fail(GDN_ERR_UNSUPPORTED, "pages_copy: too much for one launch; split the list");
   return cuda_status(gdn::launch_pages_copy(a, plain != 0, (cudaStream_t)stream), "pages_copy launch");
 }
 

@@ -131,7 +131,7 @@ struct PagesCopy {
   const int32_t* src; const int32_t* dst; int32_t n;
 };
 // plain: no destination is named twice and none is another entry's source
-bool pages_copy_fits(const PagesCopy& a);           // one launch can number its tiles
+bool pages_copy_fits(const PagesCopy& a, bool plain);      // one launch can number its tiles
 cudaError_t launch_pages_copy(const PagesCopy& a, bool plain, cudaStream_t stream);
 cudaError_t launch_pages_take(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n, int32_t* out,
                               cudaStream_t stream);

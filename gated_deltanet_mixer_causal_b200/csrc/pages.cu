@@ -7,7 +7,7 @@
 // Measured, share of the bytes at the copy rate: 200 pages of 2 MB 129 us (100 %); 256 pages of
 // 3.2 MB compacted, plan included, 69 us (90 %); one page into 8 new ones in 4 layers, with the
 // taking of the pages, 25 us (70 %; writes alone are 17 us); 64 beams of 1.1 MB in 4 layers
-// reordered in place 96 us (72 %: short runs of every page in turn, see below).
+// reordered in place 83 us (84 %: short runs of every page in turn, see below).
 #include <atomic>
 
 #include "common.cuh"
@@ -16,7 +16,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kCopyThreads = 512, kPlainThreads = 256;
+constexpr int kPlainThreads = 256;
 constexpr int kPlainLog = 14;           // log2 of a plain tile's bytes
 constexpr int kPlanThreads = 1024;
 
@@ -49,23 +49,19 @@ template <int WARPS> __device__ __forceinline__ int block_scan(int v, int* warp_
 // ------------------------------------------------------------------------------- copy
 //
 // Entry i moves page src[i] to page dst[i], as if every source were read before any destination
-// is written. Bound by HBM. Two kernels:
+// is written. Bound by HBM. A CTA copies a tile, its loads into registers before its stores. Tiles
+// are not looped over by resident CTAs: taken up in the order of the pages by the hardware's
+// scheduler, they keep the reads and writes of the moment close together (419 MB copied: 127 us,
+// 6.6 TB/s; by a grid of resident CTAs that stride over the tiles 145 us, by bulk copies through
+// shared memory 138 us).
 //
-// Where the caller knows that no destination repeats and none is another entry's source (plain),
-// one CTA copies one tile of 16 KB. The tiles are not looped over by resident CTAs: taken up in
-// the order of the pages by the hardware's scheduler, they keep the reads and writes of the moment
-// close together (419 MB copied: 127 us, 6.6 TB/s; by a grid of resident CTAs that stride over the
-// tiles 145 us, by bulk copies through shared memory 138 us).
-//
-// Else each CTA first works the list out for itself: a hash table of the destinations in shared
-// memory gives the last entry of each (the one that counts) and tells whether some source is a
-// destination too. That costs each CTA about 2 us, so the CTAs are resident and loop over tiles.
-// A tile's loads go to registers, then, behind a barrier, its stores. In a list without such
-// sources a tile is a run of columns of one page; else it takes its columns of ALL entries, so
-// that no other CTA touches them and the barrier is the only order needed.
-
-// log2 of a tile's bytes: U 16-byte words of every thread
-__host__ __device__ constexpr int copy_tile_log(int U) { return U == 8 ? 16 : 14; }
+// Where the caller knows that no destination repeats and none is another entry's source (plain), a
+// tile is a run of 16 KB of one page. Else it is a column of ALL entries, so that no other CTA
+// touches its bytes and the barrier between its loads and its stores is the only order needed; a
+// hash table of the destinations in shared memory, made by each CTA for itself, gives the last
+// entry of each, the one that counts. There the run of one page is a tile's bytes by the entries
+// (512 of 32 KB, 1 KB of 64 KB for 64 entries), and short runs cost bandwidth: 64 chained pages of
+// 2 MB 5.6 TB/s, 256 6.1, 1,000 of 256 KB 3.5, 2,000 of them (32-byte runs) 2.0.
 
 struct Table {
   int32_t* key;    // destination page, -1: empty
@@ -85,97 +81,74 @@ __device__ __forceinline__ int find(const Table& t, int32_t page) {
   }
 }
 
-template <int U>
-__global__ void __launch_bounds__(kCopyThreads, 2)
-pages_copy_kernel(const PagesCopy a, uint32_t slots) {
+// log2 of a tile's bytes: U 16-byte words of each of T threads
+__host__ __device__ constexpr int tile_log(int T, int U) {
+  int log = 4;
+  while (16 << (log - 4) < T * U * 16) ++log;
+  return log;
+}
+
+// first[k]: the first CTA of pool k
+struct CopyTiles { uint32_t first[kPagesMaxPools]; };
+
+__device__ __forceinline__ int pool_of(const CopyTiles& t, int n_pools) {
+  int k = 0;
+  while (k + 1 < n_pools && blockIdx.x >= t.first[k + 1]) ++k;
+  return k;
+}
+
+template <int T, int U>
+__global__ void __launch_bounds__(T, 1024 / T)
+pages_copy_kernel(const PagesCopy a, const CopyTiles t, uint32_t slots, int log_n) {
   extern __shared__ int32_t sm[];
   Table tab{sm, sm + slots, slots - 1};
+  int32_t* ms = sm + 2 * slots;       // [n] sources, -1: the entry does not count
+  int32_t* md = ms + a.n;
   wait_for_previous_grid();
-  int32_t* ms = sm + 2 * slots;       // [n] sources of the entries that count
-  int32_t* md = ms + a.n;             // [n] their destinations
-  __shared__ int sums[32], chained;
-  constexpr int K = kPagesMaxList / kCopyThreads;
-  int32_t es[K], ed[K];               // this thread's entries, i = k * kCopyThreads + threadIdx.x
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int i = k * kCopyThreads + threadIdx.x;
-    es[k] = i < a.n ? a.src[i] : -1;
-    ed[k] = i < a.n ? a.dst[i] : -1;
-  }
-  if (threadIdx.x == 0) chained = 0;
-  for (uint32_t s = threadIdx.x; s < slots; s += kCopyThreads) { tab.key[s] = -1; tab.val[s] = -1; }
+  for (uint32_t h = threadIdx.x; h < slots; h += T) { tab.key[h] = -1; tab.val[h] = -1; }
   __syncthreads();
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if (es[k] < 0 || es[k] >= a.src_pages || ed[k] < 0 || ed[k] >= a.dst_pages) { ed[k] = -1; continue; }
-    uint32_t h = slot_of(ed[k], tab.mask);
+  for (int i = threadIdx.x; i < a.n; i += T) {
+    const int32_t s = a.src[i], d = a.dst[i];
+    const bool in = s >= 0 && s < a.src_pages && d >= 0 && d < a.dst_pages;
+    ms[i] = in ? s : -1;
+    md[i] = d;
+    if (!in) continue;
+    uint32_t at = slot_of(d, tab.mask);
     while (true) {
-      const int32_t was = atomicCAS(&tab.key[h], -1, ed[k]);
-      if (was == -1 || was == ed[k]) break;
-      h = (h + 1) & tab.mask;
+      const int32_t was = atomicCAS(&tab.key[at], -1, d);
+      if (was == -1 || was == d) break;
+      at = (at + 1) & tab.mask;
     }
-    atomicMax(&tab.val[h], k * kCopyThreads + (int)threadIdx.x);
+    atomicMax(&tab.val[at], i);
   }
   __syncthreads();
-  // the entries that count, in the list's order: every CTA must number them alike
-  int m = 0;
+  for (int i = threadIdx.x; i < a.n; i += T)
+    if (ms[i] >= 0 && find(tab, md[i]) != i) ms[i] = -1;
+  __syncthreads();
+  constexpr int kLog = tile_log(T, U);
+  const int k = pool_of(t, a.n_pools);
+  const PagePool& p = a.pool[k];
+  const int lw = kLog - log_n, lu = lw - 4;
+  const uint32_t cta = blockIdx.x - t.first[k], cols = (uint32_t)((p.page_bytes + (1LL << lw) - 1) >> lw), layer = cta / cols;
+  const int64_t col = (int64_t)(cta - layer * cols) << lw, left = p.page_bytes - col;
+  const char* from = p.src + layer * p.src_layer + col;
+  char* to = p.dst + layer * p.dst_layer + col;
+  uint4 v[U];
+  int32_t e[U];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if (k * kCopyThreads >= a.n) break;
-    const bool on = ed[k] >= 0 && find(tab, ed[k]) == k * kCopyThreads + (int)threadIdx.x;
-    int total;
-    const int at = m + block_scan<kCopyThreads / 32>(on, sums, total);
-    if (on) {
-      ms[at] = es[k]; md[at] = ed[k];
-      if (es[k] != ed[k] && find(tab, es[k]) >= 0) chained = 1;
-    }
-    m += total;
+  for (int u = 0; u < U; ++u) {
+    const int idx = u * T + threadIdx.x, off = (idx & ((1 << lu) - 1)) << 4;
+    e[u] = idx >> lu;
+    int32_t m = -1;
+    if (e[u] < a.n && off < left) m = ms[e[u]];
+    if (m < 0) e[u] = -1;
+    else v[u] = *reinterpret_cast<const uint4*>(from + m * p.src_page + off);
   }
   __syncthreads();
-  if (m == 0) return;
-
-  constexpr int kLog = copy_tile_log(U);
-  uint32_t first = 0;                                              // this pool's first tile
-  for (int k = 0; k < a.n_pools; ++k) {
-    const PagePool& p = a.pool[k];
-    // the tile: 2^lm entries x 2^lw bytes
-    const bool clash = p.same && chained;
-    int lw;
-    if (clash) {
-      for (lw = kLog; lw > 4 && ((int64_t)m << lw) > (1 << kLog);) --lw;
-    } else {
-      for (lw = 4; (1LL << lw) < p.page_bytes && lw < kLog;) ++lw;
-    }
-    const int lm = kLog - lw, lu = lw - 4;
-    const uint32_t cols = (uint32_t)((p.page_bytes + (1LL << lw) - 1) >> lw), groups = ((uint32_t)(m - 1) >> lm) + 1;
-    const uint32_t tiles = cols * groups * p.layers;
-    uint32_t tile = (blockIdx.x + gridDim.x - first % gridDim.x) % gridDim.x;   // the pools' tiles in one round
-    first += tiles;
-    for (; tile < tiles; tile += gridDim.x) {
-      const uint32_t rest = tile / cols, layer = rest / groups, grp = rest - layer * groups;
-      const int64_t col = (int64_t)(tile - rest * cols) << lw;
-      const char* from = p.src + layer * p.src_layer + col;
-      char* to = p.dst + layer * p.dst_layer + col;
-      const int64_t left = p.page_bytes - col;                     // bytes of a page from this column on
-      uint4 v[U];
-      int32_t e[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int idx = u * kCopyThreads + threadIdx.x;
-        const int off = (idx & ((1 << lu) - 1)) << 4;
-        e[u] = (int)(grp << lm) + (idx >> lu);
-        int32_t s = -1;
-        if (e[u] < m && off < left) s = ms[e[u]];
-        if (s < 0) e[u] = -1;
-        else v[u] = *reinterpret_cast<const uint4*>(from + s * p.src_page + off);
-      }
-      if (clash) __syncthreads();
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int off = ((u * kCopyThreads + threadIdx.x) & ((1 << lu) - 1)) << 4;
-        if (e[u] >= 0) __stcs(reinterpret_cast<uint4*>(to + md[e[u]] * p.dst_page + off), v[u]);
-      }
-    }
+  for (int u = 0; u < U; ++u) {
+    const int off = ((u * T + threadIdx.x) & ((1 << lu) - 1)) << 4;
+    if (e[u] >= 0) *reinterpret_cast<uint4*>(to + md[e[u]] * p.dst_page + off) = v[u];
   }
 }
 
@@ -199,15 +172,11 @@ __host__ __device__ inline PlainShape plain_shape(int64_t page_bytes, int n) {
   return s;
 }
 
-// first[k]: the first CTA of pool k
-struct CopyTiles { uint32_t first[kPagesMaxPools]; };
-
 __global__ void __launch_bounds__(kPlainThreads, 6)
 pages_copy_plain_kernel(const PagesCopy a, const CopyTiles t) {
   constexpr int U = (1 << kPlainLog) / (kPlainThreads * 16);
   wait_for_previous_grid();
-  int k = 0;
-  while (k + 1 < a.n_pools && blockIdx.x >= t.first[k + 1]) ++k;
+  const int k = pool_of(t, a.n_pools);
   const PagePool& p = a.pool[k];
   const PlainShape sh = plain_shape(p.page_bytes, a.n);
   const uint32_t cta = blockIdx.x - t.first[k], rest = cta / sh.cols, layer = rest / sh.step;
@@ -332,61 +301,66 @@ pages_plan_kernel(int32_t* refs, int32_t n_pages, int32_t* table, int32_t n_tabl
   if (threadIdx.x == 0) *n_live = live_all;
 }
 
-// Tiles of a call by the general kernel at most, when every entry counts.
-int64_t copy_tiles(const PagesCopy& a, int log) {
-  int64_t tiles = 0;
-  for (int k = 0; k < a.n_pools; ++k)
-    tiles += (((a.pool[k].page_bytes + 15) >> 4) * a.n * a.pool[k].layers + (1 << (log - 4)) - 1) >> (log - 4);
-  return tiles;
+// CTAs of a call, and the first of each pool.
+int64_t plain_ctas(const PagesCopy& a, CopyTiles& t) {
+  int64_t ctas = 0;
+  for (int k = 0; k < a.n_pools; ++k) {
+    const PlainShape s = plain_shape(a.pool[k].page_bytes, a.n);
+    t.first[k] = (uint32_t)ctas;
+    ctas += (int64_t)s.cols * s.step * a.pool[k].layers;
+  }
+  return ctas;
 }
 
-int64_t plain_ctas(const PagePool& p, int n) {
-  const PlainShape s = plain_shape(p.page_bytes, n);
-  return (int64_t)s.cols * s.step * p.layers;
+int log_of(int n) {
+  int log = 0;
+  while ((1 << log) < n) ++log;
+  return log;
 }
 
-template <int U>
-cudaError_t launch_copy(const PagesCopy& a, int sms, cudaStream_t st) {
-  uint32_t slots = 32;
-  while (slots < 2u * (uint32_t)a.n) slots *= 2;
-  const size_t smem = sizeof(int32_t) * (2 * (size_t)slots + 2 * (size_t)a.n);
+int64_t general_ctas(const PagesCopy& a, int log_tile, CopyTiles& t) {
+  const int lw = log_tile - log_of(a.n);
+  int64_t ctas = 0;
+  for (int k = 0; k < a.n_pools; ++k) {
+    t.first[k] = (uint32_t)ctas;
+    ctas += ((a.pool[k].page_bytes + (1LL << lw) - 1) >> lw) * a.pool[k].layers;
+  }
+  return ctas;
+}
+
+template <int T, int U>
+cudaError_t launch_general(const PagesCopy& a, cudaStream_t st) {
+  CopyTiles t{};
+  const int64_t ctas = general_ctas(a, tile_log(T, U), t);
+  const uint32_t slots = 2u << log_of(a.n < 16 ? 16 : a.n);
+  const size_t smem = 8 * ((size_t)slots + a.n);
   static std::atomic<uint64_t> prepared{0};
-  const cudaError_t e = raise_smem_limit(pages_copy_kernel<U>, 64 * 1024, prepared);
+  const cudaError_t e = raise_smem_limit(pages_copy_kernel<T, U>, 64 * 1024, prepared);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = copy_tiles(a, copy_tile_log(U)) + a.n_pools;
-  return launch_overlapped(pages_copy_kernel<U>, dim3((unsigned)(tiles < sms * 2 ? tiles : sms * 2)), dim3(kCopyThreads),
-                           smem, st, a, slots);
+  return launch_overlapped(pages_copy_kernel<T, U>, dim3((unsigned)ctas), dim3(T), smem, st, a, t, slots, log_of(a.n));
 }
+
+// The general form's two tiles: 32 KB by 256 threads up to 128 entries (64 pages of 2 MB 48 us, 128
+// 91; by 64 KB 47 and 98), 64 KB by 512 threads beyond (256 of them 176 us, by 32 KB 187; 1,000 of
+// 256 KB 149, by 32 KB 284).
+constexpr int kSmallList = 128;
+static_assert(kPagesMaxList << 4 <= 1 << tile_log(512, 8), "a tile holds 16 bytes of every entry");
 
 }  // namespace
 
-bool pages_copy_fits(const PagesCopy& a) {
-  int64_t tiles = 0;
-  for (int k = 0; k < a.n_pools; ++k) tiles += plain_ctas(a.pool[k], a.n);
-  return tiles <= 0x7fffffffLL && copy_tiles(a, 4) <= 0xffffffffLL * 64;
+bool pages_copy_fits(const PagesCopy& a, bool plain) {
+  CopyTiles t;
+  const int64_t ctas = plain ? plain_ctas(a, t) : general_ctas(a, a.n <= kSmallList ? tile_log(256, 8) : tile_log(512, 8), t);
+  return ctas <= 0x7fffffffLL;
 }
 
 cudaError_t launch_pages_copy(const PagesCopy& a, bool plain, cudaStream_t st) {
   if (plain) {
     CopyTiles t{};
-    int64_t tiles = 0;
-    for (int k = 0; k < a.n_pools; ++k) {
-      t.first[k] = (uint32_t)tiles;
-      tiles += plain_ctas(a.pool[k], a.n);
-    }
-    return launch_overlapped(pages_copy_plain_kernel, dim3((unsigned)tiles), dim3(kPlainThreads), 0, st, a, t);
+    const int64_t ctas = plain_ctas(a, t);
+    return launch_overlapped(pages_copy_plain_kernel, dim3((unsigned)ctas), dim3(kPlainThreads), 0, st, a, t);
   }
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  // Large tiles keep more loads in flight and, where entries depend on one another, take longer
-  // runs of each page (200 chained pages of 2 MB: 163 us by 64 KB tiles, 201 by 32 KB, 307 by
-  // 16 KB); small ones spread a short copy over more SMs (one such page: 4.4 us by 16 KB, 5.7 by
-  // 64). A tile must hold 16 bytes of every entry: 1,024 entries by 16 KB, 4,096 by 64 KB.
-  static_assert(kPagesMaxList << 4 <= 1 << copy_tile_log(8), "a tile holds the longest list");
-  if (a.n <= 256 && copy_tiles(a, copy_tile_log(8)) < 2 * sms) return launch_copy<2>(a, sms, st);
-  return launch_copy<8>(a, sms, st);
+  return a.n <= kSmallList ? launch_general<256, 8>(a, st) : launch_general<512, 8>(a, st);
 }
 
 cudaError_t launch_pages_take(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n, int32_t* out,
