@@ -17,6 +17,8 @@
 // up dw and the fp32 instructions of two sigmoid factors an element take the rest); add norm
 // backward 16,384 x 4,096 with an fp32 residual 172 us (95 %). A decode batch of 64 tokens takes
 // 2.8 and 2.4 us, of which a launch is about 2.
+#include <atomic>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -38,41 +40,60 @@ template <int LANES> __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// VEC elements as they lie in memory: loads that are ahead of their use hold half the registers
-// that bf16 values widened to fp32 would.
+// VEC elements (whole 16-byte words) as they lie in memory: loads that are ahead of their use hold
+// half the registers that bf16 values widened to fp32 would.
 template <typename T, int VEC> struct Raw {
-  static constexpr int kBytes = VEC * (int)sizeof(T);
-  static constexpr int kWords = kBytes >= 16 ? kBytes / 16 : 1;
+  static constexpr int kWords = VEC * (int)sizeof(T) / 16, kPer = 16 / (int)sizeof(T);
   uint4 u[kWords];
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (kBytes >= 16) {
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
-    } else {
-      static_assert(VEC == 1, "single elements or whole 16-byte words");
-      if constexpr (sizeof(T) == 4) u[0].x = *reinterpret_cast<const uint32_t*>(p);
-      else u[0].x = *reinterpret_cast<const uint16_t*>(p);
-    }
+    for (int i = 0; i < kWords; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) u[i] = make_uint4(0, 0, 0, 0);
   }
+  // the elements [from, to) of the run one by one, zeros for the others
+  __device__ __forceinline__ void load_part(const T* p, int from, int to) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int e = i * kPer + j;
+        if (e < from || e >= to) continue;
+        if constexpr (sizeof(T) == 4) w[j] = reinterpret_cast<const uint32_t*>(p)[e];
+        else w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (j % 2 * 16);
+      }
+      u[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  // zeros outside [from, to)
+  __device__ __forceinline__ void keep(int from, int to) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      uint32_t m[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int e = i * kPer + j;
+        const uint32_t on = e >= from && e < to ? 0xFFFFFFFFu : 0u;
+        if constexpr (sizeof(T) == 4) m[j] = on;
+        else m[j / 2] |= on & (j % 2 ? 0xFFFF0000u : 0xFFFFu);
+      }
+      u[i].x &= m[0]; u[i].y &= m[1]; u[i].z &= m[2]; u[i].w &= m[3];
+    }
+  }
   __device__ __forceinline__ void get(float (&f)[VEC]) const {
-    if constexpr (VEC == 1) {
-      f[0] = __uint_as_float(sizeof(T) == 4 ? u[0].x : u[0].x << 16);
-    } else {
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+    for (int i = 0; i < kWords; ++i) {
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (sizeof(T) == 4) {
-            f[i * 4 + j] = __uint_as_float(w[j]);
-          } else {
-            f[i * 8 + 2 * j] = __uint_as_float(w[j] << 16);
-            f[i * 8 + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-          }
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) {
+          f[i * 4 + j] = __uint_as_float(w[j]);
+        } else {
+          f[i * 8 + 2 * j] = __uint_as_float(w[j] << 16);
+          f[i * 8 + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
         }
       }
     }
@@ -226,14 +247,62 @@ norm_dw_kernel(const float* __restrict__ part, int n_part, int D, float* __restr
 
 // -------------------------------------------------------------------------- add norm
 //
-// blockDim = (threads a row, rows a CTA); a thread holds NV runs of VEC elements of its row,
-// run k at column (k * blockDim.x + threadIdx.x) * VEC.
+// blockDim = (threads a row, rows a CTA); a thread holds NV runs of 8 elements of its row. All
+// tensors of rows lie alike, so a run that is aligned in one is aligned in all. Where D is not a
+// multiple of 8 (ODD) a row begins `lead` elements behind a run's boundary: its first and last run
+// are partly the neighbours'. They are read whole, but for the first and the last of the tensor, and
+// written element by element. A thread's rows are a multiple of 8 apart, so that `lead`, and with it
+// the thread's columns of w and dw, stays the same.
+
+constexpr int kRun = 8;
+
+template <bool ODD> struct Columns {
+  int lead, D;
+  int64_t rows;
+  __device__ __forceinline__ Columns(int64_t row, int64_t rows_, int D_)
+      : lead(ODD ? (int)((row * D_) & (kRun - 1)) : 0), D(D_), rows(rows_) {}
+  __device__ __forceinline__ int at(int k) const { return (k * (int)blockDim.x + (int)threadIdx.x) * kRun - lead; }
+  template <typename T> __device__ __forceinline__ void load(Raw<T, kRun>& r, const T* base, int64_t row, int c) const {
+    const T* p = base + row * D + c;
+    if (c + kRun <= D && (!ODD || c >= 0)) {
+      r.load(p);
+    } else if (ODD && c < D && c > -kRun) {
+      if ((c >= 0 || row > 0) && (c + kRun <= D || row + 1 < rows)) { r.load(p); r.keep(-c, D - c); }
+      else r.load_part(p, -c, D - c);
+    } else {
+      r.zero();
+    }
+  }
+  // of a vector that begins at column 0, whatever the row's lead
+  template <typename T> __device__ __forceinline__ void load_w(Raw<T, kRun>& r, const T* w, int c) const {
+    if (!ODD) load(r, w, 0, c);
+    else if (c < D && c > -kRun) r.load_part(w + c, -c, D - c);
+    else r.zero();
+  }
+  template <typename T> __device__ __forceinline__ void store(T* base, int64_t row, int c, const float (&v)[kRun]) const {
+    T* p = base + row * D + c;
+    if (c + kRun <= D && (!ODD || c >= 0)) {
+      VecIO<T, kRun>::store(p, v);
+    } else if (ODD && c < D && c > -kRun) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i)
+        if (c + i >= 0 && c + i < D) p[i] = from_f<T>(v[i]);
+    }
+  }
+};
 
 // Sums of v and u over the threads of a row; every thread of the CTA calls it. The first exchange
 // of a warp leaves v's half sums in its lower lanes and u's in its upper ones, so one tree of
 // shuffles serves both. sm holds two buffers that successive calls use in turn (`turn`), so one
 // barrier a call is enough: a buffer is written again only behind the next call's barrier.
 __device__ __forceinline__ float2 row_sum(float v, float u, float (*sm)[64], int turn) {
+  if (blockDim.x < 32) {                 // a few rows a warp
+    for (int m = blockDim.x >> 1; m >= 1; m >>= 1) {
+      v += __shfl_xor_sync(0xffffffffu, v, m);
+      u += __shfl_xor_sync(0xffffffffu, u, m);
+    }
+    return make_float2(v, u);
+  }
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const bool up = lane & 16;
   float a = (up ? u : v) + __shfl_xor_sync(0xffffffffu, up ? v : u, 16);
@@ -250,104 +319,106 @@ __device__ __forceinline__ float2 row_sum(float v, float u, float (*sm)[64], int
   return make_float2(__shfl_sync(0xffffffffu, a, 0), __shfl_sync(0xffffffffu, a, 16));
 }
 
-template <typename T, typename R, int VEC, int NV, int MAXT>
+template <typename T, typename R, int NV, int MAXT, bool ODD>
 __global__ void __launch_bounds__(MAXT)
 add_norm_kernel(const T* __restrict__ x, const R* res, const T* __restrict__ w, float scale, float w_add, float eps,
                 R* h, T* __restrict__ n, int64_t rows, int D) {
   __shared__ float sm[2][64];
   allow_next_grid();
   wait_for_previous_grid();
-  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const bool live = row < rows;
-  float v[NV][VEC], ss = 0.f;
-  Raw<T, VEC> wv[NV];
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const Columns<ODD> cols(row, rows, D);
+  Raw<T, kRun> wv[NV];
+  if (ODD) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int c = (k * blockDim.x + threadIdx.x) * VEC;
-    Raw<T, VEC> xr;
-    Raw<R, VEC> rr;
-    xr.zero(); rr.zero(); wv[k].zero();
-    if (live && c < D) {
-      xr.load(x + row * D + c);
-      rr.load(res + row * D + c);
-      wv[k].load(w + c);
-    }
-    float xv[VEC];
-    xr.get(xv); rr.get(v[k]);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      v[k][i] = fmaf(scale, xv[i], v[k][i]);
-      ss = fmaf(v[k][i], v[k][i], ss);
-    }
+    for (int k = 0; k < NV; ++k) cols.load_w(wv[k], w, cols.at(k));
   }
-  const float rstd = rsqrtf(row_sum(ss, 0.f, sm, 0).x * (1.0f / D) + eps);
+  int turn = 0;
+  do {
+    const bool live = row < rows;
+    float v[NV][kRun], ss = 0.f;
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int c = (k * blockDim.x + threadIdx.x) * VEC;
-    if (live && c < D) {
-      VecIO<R, VEC>::store(h + row * D + c, v[k]);
-      float wf[VEC];
-      wv[k].get(wf);
+    for (int k = 0; k < NV; ++k) {
+      Raw<T, kRun> xr;
+      Raw<R, kRun> rr;
+      xr.zero(); rr.zero();
+      if (live) { cols.load(xr, x, row, cols.at(k)); cols.load(rr, res, row, cols.at(k)); }
+      if (!ODD) cols.load_w(wv[k], w, cols.at(k));
+      float xv[kRun];
+      xr.get(xv); rr.get(v[k]);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[k][i] *= rstd * (wf[i] + w_add);
-      VecIO<T, VEC>::store(n + row * D + c, v[k]);
+      for (int i = 0; i < kRun; ++i) {
+        v[k][i] = fmaf(scale, xv[i], v[k][i]);
+        ss = fmaf(v[k][i], v[k][i], ss);
+      }
     }
-  }
+    const float rstd = rsqrtf(row_sum(ss, 0.f, sm, turn++).x * (1.0f / D) + eps);
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        cols.store(h, row, cols.at(k), v[k]);
+        float wf[kRun];
+        wv[k].get(wf);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) v[k][i] *= rstd * (wf[i] + w_add);
+        cols.store(n, row, cols.at(k), v[k]);
+      }
+    }
+    row += (int64_t)gridDim.x * blockDim.y;
+  } while (ODD && row - threadIdx.y < rows);      // aligned rows have a CTA each
 }
 
 // A CTA takes every gridDim.x-th group of rows; a thread keeps its columns' weight gradient in
 // registers over them and has the next row's loads in flight while it works on one.
-template <typename T, typename R, int VEC, int NV, int MAXT, int MINB>
+template <typename T, typename R, int NV, int MAXT, int MINB, bool ODD>
 __global__ void __launch_bounds__(MAXT, MINB)
 add_norm_bwd_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* __restrict__ dn, const R* dh,
                     float scale, float w_add, float eps, R* dres, T* __restrict__ dx,
                     float* __restrict__ part, int64_t rows, int D) {
   __shared__ float sm[2][64];
+  extern __shared__ float sum_w[];          // [D] where several rows share a CTA
   wait_for_previous_grid();
   const float inv_d = 1.0f / D;
-  float dw[NV][VEC];
-  Raw<T, VEC> wv[NV], dr[NV];
-  Raw<R, VEC> hr[NV], gr[NV];
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int c = (k * blockDim.x + threadIdx.x) * VEC;
-    wv[k].zero();
-    if (c < D) wv[k].load(w + c);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) dw[k][i] = 0.f;
-  }
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const Columns<ODD> cols(row, rows, D);
+  float dw[NV][kRun];
+  Raw<T, kRun> wv[NV], dr[NV];
+  Raw<R, kRun> hr[NV], gr[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    cols.load_w(wv[k], w, cols.at(k));
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) dw[k][i] = 0.f;
+  }
   auto fetch_row = [&](int64_t r) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (k * blockDim.x + threadIdx.x) * VEC;
       hr[k].zero(); dr[k].zero();
-      if (r < rows && c < D) { hr[k].load(h + r * D + c); dr[k].load(dn + r * D + c); }
+      if (r < rows) { cols.load(hr[k], h, r, cols.at(k)); cols.load(dr[k], dn, r, cols.at(k)); }
     }
   };
   auto fetch_dh = [&](int64_t r) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (k * blockDim.x + threadIdx.x) * VEC;
       gr[k].zero();
-      if (dh && r < rows && c < D) gr[k].load(dh + r * D + c);
+      if (dh && r < rows) cols.load(gr[k], dh, r, cols.at(k));
     }
   };
   fetch_row(row);
   fetch_dh(row);
   int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < rows; r0 += step, row += step, ++turn) {
-    float hv[NV][VEC], da[NV][VEC], ss = 0.f, ax = 0.f;
+  for (int64_t r0 = row - threadIdx.y; r0 < rows; r0 += step, row += step, ++turn) {
+    float hv[NV][kRun], da[NV][kRun], ss = 0.f, ax = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) { hr[k].get(hv[k]); dr[k].get(da[k]); }
     fetch_row(row + step);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      float wf[VEC];
+      float wf[kRun];
       wv[k].get(wf);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
+      for (int i = 0; i < kRun; ++i) {
         ss = fmaf(hv[k][i], hv[k][i], ss);
         ax = fmaf(da[k][i] * (wf[i] + w_add), hv[k][i], ax);
       }
@@ -356,21 +427,20 @@ add_norm_bwd_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* _
     const float r1 = rsqrtf(fmaf(s.x, inv_d, eps)), cc = -s.y * r1 * r1 * inv_d;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (k * blockDim.x + threadIdx.x) * VEC;
-      float wf[VEC], gv[VEC];
+      float wf[kRun], gv[kRun];
       wv[k].get(wf);
       gr[k].get(gv);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
+      for (int i = 0; i < kRun; ++i) {
         dw[k][i] = fmaf(da[k][i], hv[k][i] * r1, dw[k][i]);
         gv[i] = fmaf(r1, fmaf(da[k][i], wf[i] + w_add, cc * hv[k][i]), gv[i]);
       }
-      if (row < rows && c < D) {
-        VecIO<R, VEC>::store(dres + row * D + c, gv);
+      if (row < rows) {
+        cols.store(dres, row, cols.at(k), gv);
         if (dx) {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) gv[i] *= scale;
-          VecIO<T, VEC>::store(dx + row * D + c, gv);
+          for (int i = 0; i < kRun; ++i) gv[i] *= scale;
+          cols.store(dx, row, cols.at(k), gv);
         }
       }
     }
@@ -378,80 +448,183 @@ add_norm_bwd_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* _
   }
   if (part == nullptr) return;
   allow_next_grid();
-  // the rows of the CTA take their turns at one row of parts
   float* mine = part + (int64_t)blockIdx.x * D;
-  for (int y = 0; y < blockDim.y; ++y) {
-    if (threadIdx.y == y) {
+  if (blockDim.y == 1) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int c = (k * blockDim.x + threadIdx.x) * VEC;
-        if (c < D) {
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) mine[c + i] = y ? mine[c + i] + dw[k][i] : dw[k][i];
-        }
+      for (int i = 0; i < kRun; ++i) {
+        const int c = cols.at(k) + i;
+        if (c >= 0 && c < D) mine[c] = dw[k][i];
+      }
+    return;
+  }
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
+  for (int c = tid; c < D; c += threads) sum_w[c] = 0.f;
+  for (int y = 0; y < blockDim.y; ++y) {    // the rows of the CTA in turn
+    __syncthreads();
+    if (threadIdx.y != y) continue;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const int c = cols.at(k) + i;
+        if (c >= 0 && c < D) sum_w[c] += dw[k][i];
+      }
+  }
+  __syncthreads();
+  for (int c = tid; c < D; c += threads) mine[c] = sum_w[c];
+}
+
+// Rows too long for registers: a CTA reads its row twice, the second time from the caches, and
+// keeps the weight gradient in shared memory.
+template <typename T, typename R, bool ODD>
+__global__ void __launch_bounds__(1024, 1)
+add_norm_bwd_long_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* __restrict__ dn, const R* dh,
+                         float scale, float w_add, float eps, R* dres, T* __restrict__ dx,
+                         float* __restrict__ part, int64_t rows, int D) {
+  __shared__ float sm[2][64];
+  extern __shared__ float sum_w[];          // [runs * 8], from the first run's first column
+  wait_for_previous_grid();
+  const float inv_d = 1.0f / D;
+  const Columns<ODD> cols(blockIdx.x, rows, D);
+  const int runs = (D + cols.lead + kRun - 1) / kRun, nv = (runs + blockDim.x - 1) / blockDim.x;
+  for (int c = threadIdx.x; c < runs * kRun; c += blockDim.x) sum_w[c] = 0.f;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, ++turn) {
+    float ss = 0.f, ax = 0.f;
+    for (int k = 0; k < nv; ++k) {
+      Raw<R, kRun> hr;
+      Raw<T, kRun> dr, wr;
+      cols.load(hr, h, row, cols.at(k)); cols.load(dr, dn, row, cols.at(k)); cols.load_w(wr, w, cols.at(k));
+      float hv[kRun], da[kRun], wf[kRun];
+      hr.get(hv); dr.get(da); wr.get(wf);
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        ss = fmaf(hv[i], hv[i], ss);
+        ax = fmaf(da[i] * (wf[i] + w_add), hv[i], ax);
       }
     }
-    __syncthreads();
+    const float2 s = row_sum(ss, ax, sm, turn);
+    const float r1 = rsqrtf(fmaf(s.x, inv_d, eps)), cc = -s.y * r1 * r1 * inv_d;
+    for (int k = 0; k < nv; ++k) {
+      const int c = cols.at(k);
+      if (c >= D) break;
+      Raw<R, kRun> hr, gr;
+      Raw<T, kRun> dr, wr;
+      cols.load(hr, h, row, c); cols.load(dr, dn, row, c); cols.load_w(wr, w, c);
+      gr.zero();
+      if (dh) cols.load(gr, dh, row, c);
+      float hv[kRun], da[kRun], wf[kRun], gv[kRun];
+      hr.get(hv); dr.get(da); wr.get(wf); gr.get(gv);
+      float* mw = sum_w + c + cols.lead;
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        mw[i] = fmaf(da[i], hv[i] * r1, mw[i]);
+        gv[i] = fmaf(r1, fmaf(da[i], wf[i] + w_add, cc * hv[i]), gv[i]);
+      }
+      cols.store(dres, row, c, gv);
+      if (dx) {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) gv[i] *= scale;
+        cols.store(dx, row, c, gv);
+      }
+    }
   }
+  if (part == nullptr) return;
+  allow_next_grid();
+  __syncthreads();
+  for (int c = threadIdx.x; c < D; c += blockDim.x) part[(int64_t)blockIdx.x * D + c] = sum_w[c + cols.lead];
 }
 
 struct AddShape { int tx, ty; };
 
-// Threads a row when each holds nv runs of vec elements, in whole warps; rows narrower than 256
-// threads share a CTA.
-AddShape add_shape(int D, int vec, int nv) {
-  const int runs = (D + vec - 1) / vec;
+int runs_of(int D) { return D % kRun == 0 ? D / kRun : (D + 2 * kRun - 2) / kRun; }    // with any lead
+
+// Threads a row when each holds nv runs: whole warps, or a power of two below; rows of up to 128
+// threads share a CTA of 256 (a power of two of them, see grid_of).
+AddShape add_shape(int D, int nv) {
   AddShape s;
-  s.tx = ((runs + nv - 1) / nv + 31) / 32 * 32;
-  s.ty = s.tx >= 256 ? 1 : 256 / s.tx;
+  const int threads = (runs_of(D) + nv - 1) / nv;
+  s.tx = (threads + 31) / 32 * 32;
+  if (threads <= 16)
+    for (s.tx = 1; s.tx < threads;) s.tx *= 2;
+  s.ty = s.tx > 128 ? 1 : s.tx > 64 ? 2 : s.tx > 32 ? 4 : 256 / s.tx;
   return s;
 }
 
-template <typename T, typename R, int VEC, int NV, int MAXT>
-cudaError_t add_fwd(const AddNorm& a, cudaStream_t st) {
-  const AddShape s = add_shape(a.D, VEC, NV);
-  return launch_overlapped(add_norm_kernel<T, R, VEC, NV, MAXT>, dim3((unsigned)((a.rows + s.ty - 1) / s.ty)),
-                           dim3(s.tx, s.ty), 0, st, (const T*)a.x, (const R*)a.res, (const T*)a.w, a.scale, a.w_add,
-                           a.eps, (R*)a.h, (T*)a.n, a.rows, a.D);
+// At most `most` CTAs (a multiple of 8), for odd rows a multiple of 8 of them: a thread's rows are
+// then a multiple of 8 apart. CTAs without a row add zeros.
+unsigned grid_of(int64_t groups, int64_t most, bool odd) {
+  const int64_t n = groups < most ? groups : most;
+  return (unsigned)(odd ? (n + 7) / 8 * 8 : n);
 }
 
-// MINB CTAs of the backward pass are resident on each of 148 SMs; no more are launched, so that
-// every CTA begins at once and takes the same number of rows.
-template <typename T, typename R, int VEC, int NV, int MAXT, int MINB>
-cudaError_t add_bwd(const AddNorm& a, cudaStream_t st) {
-  static_assert(MINB * 148 <= kNormParts, "parts in the workspace");
-  const AddShape s = add_shape(a.D, VEC, NV);
-  const int64_t groups = (a.rows + s.ty - 1) / s.ty;
-  const int parts = (int)(groups < MINB * 148 ? groups : MINB * 148);
-  const cudaError_t e = launch_overlapped(add_norm_bwd_kernel<T, R, VEC, NV, MAXT, MINB>, dim3(parts), dim3(s.tx, s.ty),
-                                          0, st, (const R*)a.h, (const T*)a.w, (const T*)a.n, (const R*)a.res, a.scale,
-                                          a.w_add, a.eps, (R*)a.dres, (T*)a.dx, a.dw ? a.part : nullptr, a.rows, a.D);
+template <typename T, typename R, int NV, int MAXT, bool ODD>
+cudaError_t add_fwd(const AddNorm& a, cudaStream_t st) {
+  const AddShape s = add_shape(a.D, NV);
+  // aligned rows: a CTA for each group of rows; odd ones: resident CTAs, which load w's parts once
+  const unsigned grid = grid_of((a.rows + s.ty - 1) / s.ty, ODD ? 148 * (2048 / MAXT) : 1LL << 31, ODD);
+  return launch_overlapped(add_norm_kernel<T, R, NV, MAXT, ODD>, dim3(grid), dim3(s.tx, s.ty), 0, st, (const T*)a.x,
+                           (const R*)a.res, (const T*)a.w, a.scale, a.w_add, a.eps, (R*)a.h, (T*)a.n, a.rows, a.D);
+}
+
+cudaError_t sum_parts(const AddNorm& a, cudaError_t e, int parts, cudaStream_t st) {
   return e != cudaSuccess || !a.dw ? e : launch_overlapped(norm_dw_kernel, dim3((a.D + 31) / 32), dim3(32, 32), 0, st,
                                                            a.part, parts, a.D, a.dw);
 }
 
+// MINB CTAs of the backward pass are resident on each of 148 SMs; no more are launched, so that
+// every CTA begins at once and takes the same number of rows.
+template <typename T, typename R, int NV, int MAXT, int MINB, bool ODD>
+cudaError_t add_bwd(const AddNorm& a, cudaStream_t st) {
+  static_assert(MINB * 148 <= kNormParts, "parts in the workspace");
+  const AddShape s = add_shape(a.D, NV);
+  const unsigned parts = grid_of((a.rows + s.ty - 1) / s.ty, ODD ? MINB * 148 / 8 * 8 : MINB * 148, ODD);
+  const cudaError_t e = launch_overlapped(
+      add_norm_bwd_kernel<T, R, NV, MAXT, MINB, ODD>, dim3(parts), dim3(s.tx, s.ty), s.ty > 1 ? a.D * sizeof(float) : 0,
+      st, (const R*)a.h, (const T*)a.w, (const T*)a.n, (const R*)a.res, a.scale, a.w_add, a.eps, (R*)a.dres, (T*)a.dx,
+      a.dw ? a.part : nullptr, a.rows, a.D);
+  return sum_parts(a, e, parts, st);
+}
+
+template <typename T, typename R, bool ODD>
+cudaError_t add_bwd_long(const AddNorm& a, cudaStream_t st) {
+  static std::atomic<uint64_t> prepared{0};
+  const cudaError_t p = raise_smem_limit(add_norm_bwd_long_kernel<T, R, ODD>, 96 * 1024, prepared);
+  if (p != cudaSuccess) return p;
+  const unsigned parts = grid_of(a.rows, ODD ? 144 : 148, ODD);
+  const cudaError_t e = launch_overlapped(
+      add_norm_bwd_long_kernel<T, R, ODD>, dim3(parts), dim3(1024), runs_of(a.D) * kRun * sizeof(float), st,
+      (const R*)a.h, (const T*)a.w, (const T*)a.n, (const R*)a.res, a.scale, a.w_add, a.eps, (R*)a.dres, (T*)a.dx,
+      a.dw ? a.part : nullptr, a.rows, a.D);
+  return sum_parts(a, e, parts, st);
+}
+
+// Runs of a thread and CTAs of an SM: as few threads a row as the registers allow (their barrier and
+// shuffles are paid by all of them), as many CTAs as fit. (Backward, 16,384 x 4,096, fp32 residual:
+// two runs by 256 threads 172 us, one run by 512 226; 8,000 x 8,192, bf16: forward by 512 threads 79
+// us, by 1,024 95; 4,000 x 16,384: backward reading the row twice 198 us, by registers that spill
+// 484. Odd rows: 5,000 x 7,001, bf16: forward 66 us and backward 132, element by element 204 and
+// 588; 20,000 x 1,001 40 and 60, element by element 45 and 80.)
+template <typename T, typename R, bool ODD>
+cudaError_t add_odd(const AddNorm& a, cudaStream_t st) {
+  const int runs = runs_of(a.D);
+  if (a.back) {
+    if (runs <= 256) return add_bwd<T, R, 1, 256, 4, ODD>(a, st);
+    if (runs <= 512) return add_bwd<T, R, 2, 256, 2, ODD>(a, st);
+    if (runs <= 1024) return add_bwd<T, R, 2, 512, 1, ODD>(a, st);
+    return add_bwd_long<T, R, ODD>(a, st);
+  }
+  if (runs <= 256) return add_fwd<T, R, 1, 256, ODD>(a, st);
+  if (runs <= 512) return add_fwd<T, R, 1, 512, ODD>(a, st);
+  if (runs <= 1024) return add_fwd<T, R, 2, 512, ODD>(a, st);
+  return add_fwd<T, R, ODD ? 3 : 2, 1024, ODD>(a, st);      // an odd row may take 2,049 runs
+}
+
 template <typename T, typename R>
 cudaError_t add_tr(const AddNorm& a, cudaStream_t st) {
-  // runs of 8 elements where every row begins on a run's boundary, single elements else
-  if (a.D % 8 == 0) {
-    if (a.back) {
-      if (a.D <= 2048) return add_bwd<T, R, 8, 1, 256, 4>(a, st);
-      if (a.D <= 4096) return add_bwd<T, R, 8, 2, 256, 2>(a, st);
-      if (a.D <= 8192) return add_bwd<T, R, 8, 2, 512, 1>(a, st);
-      return add_bwd<T, R, 8, 2, 1024, 1>(a, st);
-    }
-    if (a.D <= 2048) return add_fwd<T, R, 8, 1, 256>(a, st);
-    if (a.D <= 8192) return add_fwd<T, R, 8, 1, 1024>(a, st);
-    return add_fwd<T, R, 8, 2, 1024>(a, st);
-  }
-  if (a.back) {
-    if (a.D <= 1024) return add_bwd<T, R, 1, 4, 256, 4>(a, st);
-    if (a.D <= 4096) return add_bwd<T, R, 1, 8, 512, 2>(a, st);
-    return add_bwd<T, R, 1, 16, 1024, 1>(a, st);
-  }
-  if (a.D <= 1024) return add_fwd<T, R, 1, 4, 256>(a, st);
-  if (a.D <= 4096) return add_fwd<T, R, 1, 8, 512>(a, st);
-  return add_fwd<T, R, 1, 16, 1024>(a, st);
+  return a.D % kRun == 0 ? add_odd<T, R, false>(a, st) : add_odd<T, R, true>(a, st);
 }
 
 template <typename T, int D>

@@ -113,7 +113,8 @@ def add_terms(h, w, dn, dh, scale, c, eps):
 
 @pytest.mark.parametrize("dt,res", [(BF, BF), (BF, FP), (FP, FP), (FP, BF)])
 @pytest.mark.parametrize("T,D", [(1, 1), (3, 7), (5, 64), (4, 1001), (300, 40), (129, 2048), (3, 4096), (2, 8200),
-                                 (2, 9001), (3, 16384), (700, 256)])
+                                 (2, 9001), (3, 16384), (700, 256), (17, 7001), (5000, 9), (900, 70), (5, 16383),
+                                 (310, 16380), (33, 15), (1300, 130)])
 def test_add_norm(cuda_device, dt, res, T, D):
     x, r, w, dn, dh = add_case(T, D, dt, res, T + D)
     scale, c, eps = 0.7, 1.0, 1e-5
@@ -141,6 +142,29 @@ def test_add_norm(cuda_device, dt, res, T, D):
     dx2, dres2, dw2 = gdn.gdn_add_norm_bwd(h, wd, dnd, dh2, scale=scale, w_add=c, eps=eps, dres=dh2)
     one = gdn.gdn_add_norm_bwd(h, wd, dnd, dhd, scale=scale, w_add=c, eps=eps)
     assert dres2 is dh2 and all(torch.equal(a, b) for a, b in zip((dx2, dres2, dw2), one))
+
+
+@pytest.mark.parametrize("T,D", [(3, 5), (7, 1001), (2, 8203), (9, 12), (4, 64)])
+def test_add_norm_keeps_to_its_rows(cuda_device, T, D):
+    """Rows that neither begin nor end on 16 bytes, at the end of their buffers: nothing behind them
+    is written, and what lies there (NaN) is not used."""
+    x, r, w, dn, dh = add_case(T, D, BF, FP, T + D)
+    def behind(t):                                         # t in front of 64 NaN
+        buf = torch.full((t.numel() + 64,), float("nan"), dtype=t.dtype, device=cuda_device)
+        buf[:t.numel()] = t.reshape(-1).to(cuda_device)
+        return buf, buf[:t.numel()].view(t.shape)
+    bufs, views = zip(*(behind(t) for t in (x, r, w, dn, dh, torch.zeros_like(x), torch.zeros_like(r),
+                                            torch.zeros_like(x), torch.zeros_like(r))))
+    xd, rd, wd, dnd, dhd, n, h, dx, dres = views
+    gdn.gdn_add_norm(xd, rd, wd, h=h, n=n)
+    n2, h2 = gdn.gdn_add_norm(x.to(cuda_device), r.to(cuda_device), w.to(cuda_device))
+    assert torch.equal(n, n2) and torch.equal(h, h2)
+    dwb, dw = behind(torch.zeros(D))
+    gdn.gdn_add_norm_bwd(h, wd, dnd, dhd, dres=dres, dx=dx, dw=dw)
+    one = gdn.gdn_add_norm_bwd(h2, w.to(cuda_device), dn.to(cuda_device), dh.to(cuda_device))
+    assert all(torch.equal(a, b) for a, b in zip((dx, dres, dw), one))
+    for buf, t in zip((*bufs, dwb), (*views, dw)):
+        assert torch.isnan(buf[t.numel():]).all()
 
 
 def test_gradients_against_differences(cuda_device):
