@@ -9,6 +9,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -646,6 +647,7 @@ def gdn_pages_compact(refs: torch.Tensor, table: Optional[torch.Tensor], pools, 
     return lists[2 * half:-1], lists[-1:]
 
 
+@functools.lru_cache(maxsize=None)
 def gdn_norm_bwd_workspace_size(D: int) -> int:
     """Bytes of workspace the norms' backward passes need for rows of D values."""
     return int(lib().gdn_norm_bwd_workspace_size(D))
@@ -653,7 +655,7 @@ def gdn_norm_bwd_workspace_size(D: int) -> int:
 
 def _norm_workspace(D: int, workspace: Optional[torch.Tensor], device):
     if workspace is None:
-        need = lib().gdn_norm_bwd_workspace_size(D)
+        need = gdn_norm_bwd_workspace_size(D)
         return torch.empty(need, dtype=torch.uint8, device=device), need
     _need(workspace, "workspace", device=device)
     return workspace, workspace.numel() * workspace.element_size()

@@ -362,9 +362,9 @@ gdn_status_t gdn_decode_tokens_ex(const void* x, const void* conv_w, void* conv_
  * write_pages  device int32 [B, n_tok], or NULL: the state after the last valid token goes back
  *              to read_pages[b]. A value outside [0, n_pages) stores nothing. Where two tokens of
  *              one sequence name the same page, the later one's state is kept.
- * n_valid      device int32 [B], clamped to [0, n_tok], or NULL (every token). Nothing is read,
- *              written or stored for the tokens behind it, and nothing at all for a sequence of
- *              none: its rows of o stay as they were.
+ * n_valid      device int32 [B], clamped to [0, n_tok], or NULL (every token). What lies in the
+ *              tokens behind it is not used, and nothing is written or stored for them: their
+ *              rows of o stay as they were, and all of those of a sequence of none.
  * g, beta      [B, n_tok, Hv] fp32.
  * z, norm_w    both NULL, or the gate [B, n_tok, Hv, dv] (a token every z_stride elements, 0:
  *              dense) and the weight [dv], dtype dt: o is then gdn_gated_norm's result with eps.
