@@ -173,9 +173,9 @@ int64_t smem_bytes(int n_tok, int64_t KH, int64_t G, int d, int64_t rows) {
          (int64_t)sizeof(float) * n_tok * (KH * 2 * d + rows + KH + 6 * G);
 }
 
-// N sums (over the L lanes of a row) of each lane: every exchange leaves half of the sums with
-// each lane, so that log2(L) exchanges take 7 shuffles for 8 sums instead of 24. The sums end
-// in v[0 .. N / L - 1], lane seg holding those from seg * N / L on.
+// N sums (over the L lanes of a row) of each lane: every exchange leaves half of the sums with each
+// lane, 4 shuffles for 4 sums of 8 lanes instead of 12. The sums end in v[0 .. N / L - 1] (v[0] for
+// N < L), lane seg holding those from seg * N / L on.
 template <int L, int N> __device__ __forceinline__ void scatter_sums(float* v, int seg) {
   if constexpr (L > 1 && N > 1) {
     const bool up = seg & (L / 2);
@@ -405,34 +405,34 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
     const Step* st = steps;
     float* vt = vo;
     for (int t = 0; t < nv; ++t, qt += 2 * W, st += G, vt += rows) {
-      // S k and S q of the lane's rows: first its own columns, then the row's lanes together
-      f2 acc[2 * kRows];
+      // S k of the lane's rows: first its own columns, then the row's lanes together, which leaves
+      // each lane the sums of NR rows from r0 on (two lanes of 8 the same row's). S q is added up
+      // while S k's shuffles are under way: u waits for S k only.
+      constexpr int NR = kRows > L ? kRows / L : 1, SAME = L > kRows ? L / kRows : 1;
+      const int r0 = seg * kRows / L;
+      float sk[kRows], sq[kRows];
+      auto dots = [&](const float* vec, float (&sums)[kRows]) {
+        f2 acc[kRows];
 #pragma unroll
-      for (int i = 0; i < 2 * kRows; ++i) acc[i] = 0ull;
+        for (int i = 0; i < kRows; ++i) acc[i] = 0ull;
 #pragma unroll
-      for (int j = 0; j < kSeg / 4; ++j) {
-        const ulonglong2 q4 = *reinterpret_cast<const ulonglong2*>(qt + j * 4 * L);
-        const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(qt + D + j * 4 * L);
+        for (int j = 0; j < kSeg / 4; ++j) {
+          const ulonglong2 v4 = *reinterpret_cast<const ulonglong2*>(vec + j * 4 * L);
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            acc[i] = fma2(s[i][2 * j], v4.x, acc[i]);
+            acc[i] = fma2(s[i][2 * j + 1], v4.y, acc[i]);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-          acc[i] = fma2(s[i][2 * j], k4.x, acc[i]);
-          acc[kRows + i] = fma2(s[i][2 * j], q4.x, acc[kRows + i]);
-          acc[i] = fma2(s[i][2 * j + 1], k4.y, acc[i]);
-          acc[kRows + i] = fma2(s[i][2 * j + 1], q4.y, acc[kRows + i]);
+          const float2 f = unpair(acc[i]);
+          sums[i] = f.x + f.y;
         }
-      }
-      float sums[2 * kRows];
-#pragma unroll
-      for (int i = 0; i < 2 * kRows; ++i) {
-        const float2 f = unpair(acc[i]);
-        sums[i] = f.x + f.y;
-      }
-      scatter_sums<L, 2 * kRows>(sums, seg);
-      // The lower half of a row's lanes holds S k, the upper half S q, of NR rows each from row
-      // r0 on (one lane: both, of all rows). The former make u, the latter the output.
-      constexpr int H = L > 1 ? L / 2 : 1, NR = kRows > H ? kRows / H : 1;
-      const int r0 = L > 1 ? seg % H * kRows / H : 0;
-      const bool has_q = L == 1 || seg >= H;
+        scatter_sums<L, kRows>(sums, seg);
+      };
+      dots(qt + D, sk);
+      dots(qt, sq);
       float u[NR], gam[kRows], inv[kRows];
       if constexpr (RPP <= D) {             // a pass lies in one head
         const float4 p = *reinterpret_cast<const float4*>(st + (row0 + w.row) / D);
@@ -441,7 +441,7 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
           const int r = ra + (r0 + i) * RPW;
-          u[i] = p.y * ((r < end ? vt[r] : 0.f) - p.x * sums[i]);
+          u[i] = p.y * ((r < end ? vt[r] : 0.f) - p.x * sk[i]);
         }
       } else {
 #pragma unroll
@@ -453,28 +453,24 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
           const int r = ra + (r0 + i) * RPW, rr = r < end ? r : 0;
-          u[i] = st[(row0 + rr) / D].beta * (vt[rr] - st[(row0 + rr) / D].gamma * sums[i]);
+          u[i] = st[(row0 + rr) / D].beta * (vt[rr] - st[(row0 + rr) / D].gamma * sk[i]);
         }
       }
       f2 uu[kRows];
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        const float ui = L > 1 ? __shfl_sync(0xffffffffu, u[i % NR], (lane & ~(L - 1)) + i * H / kRows) : u[i % NR];
+        const float ui = L > 1 ? __shfl_sync(0xffffffffu, u[i % NR], (lane & ~(L - 1)) + i / NR * SAME) : u[i % NR];
         uu[i] = pair(ui, ui);
       }
-      if constexpr (L > 1) {                // the upper half takes the u of its own rows
-#pragma unroll
-        for (int i = 0; i < NR; ++i) u[i] = __shfl_sync(0xffffffffu, u[i], (lane & ~(L - 1)) + seg % H);
-      }
       __syncwarp();                         // v has been read where o is written
-      if (has_q) {
+      if (seg % SAME == 0) {
         const float kq = kqs[t * KH + w.head];
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
           const int r = ra + (r0 + i) * RPW;
           if (r < end) {
             const float gm = RPP <= D ? gam[0] : st[(row0 + r) / D].gamma;
-            vt[r] = a.scale * fmaf(gm, sums[L > 1 ? i : kRows + i], u[i] * kq);
+            vt[r] = a.scale * fmaf(gm, sq[i], u[i] * kq);
           }
         }
       }

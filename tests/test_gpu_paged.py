@@ -152,7 +152,7 @@ def test_paged_equals_the_dense_decode(cuda_device):
 
 
 @pytest.mark.parametrize("B,Hk,Hv,d,n,st", [(150, 16, 32, 64, 2, FP), (160, 16, 48, 32, 3, BF), (620, 8, 8, 16, 1, FP),
-                                              (300, 16, 16, 16, 5, BF)])
+                                              (300, 16, 16, 16, 5, BF), (700, 16, 48, 16, 2, FP)])
 def test_paged_equals_the_dense_decode_for_many_narrow_heads(cuda_device, B, Hk, Hv, d, n, st):
     """Batches that fill the GPU with heads below 128, where a CTA takes several key heads."""
     c = case(cuda_device, B, n, Hk, Hv, d, BF, st, B, seed=d + n)
