@@ -594,8 +594,7 @@ cudaError_t launch_d(const PagedDecode& a, cudaStream_t st) {
   attr[1].val.clusterDim.x = C; attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, decode_paged_kernel<T, S, D>, a, C, KH);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_result(cudaLaunchKernelEx(&cfg, decode_paged_kernel<T, S, D>, a, C, KH));
 }
 
 template <typename T, typename S>

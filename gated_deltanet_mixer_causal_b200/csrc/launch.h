@@ -12,6 +12,12 @@
 
 namespace gdn {
 
+// A failed launch's error, not left behind for the next call that asks for the last one.
+inline cudaError_t launch_result(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
 // Raises a kernel's limit of dynamic shared memory on the current device, once for each device
 // (numbers below 64; others every time). `prepared` is the kernel's own.
 template <typename K>
@@ -23,7 +29,7 @@ inline cudaError_t raise_smem_limit(K kernel, int bytes, std::atomic<uint64_t>& 
   if (prepared.load(std::memory_order_relaxed) & bit) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) prepared.fetch_or(bit, std::memory_order_relaxed);
-  return e;
+  return launch_result(e);
 }
 
 // Launches a kernel that begins with wait_for_previous_grid (common.cuh), so that its launch
@@ -37,8 +43,7 @@ inline cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr; cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_result(cudaLaunchKernelEx(&cfg, kernel, P(args)...));
 }
 
 constexpr int kF32 = 0;   // GDN_F32

@@ -375,6 +375,9 @@ __global__ void __launch_bounds__(MAXT, MINB)
 add_norm_bwd_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* __restrict__ dn, const R* dh,
                     float scale, float w_add, float eps, R* dres, T* __restrict__ dx,
                     float* __restrict__ part, int64_t rows, int D) {
+  // the next row's dh is asked for with its h and dn where the registers allow (bf16), else once
+  // this row's has been used
+  constexpr bool kEarly = sizeof(R) == 2;
   __shared__ float sm[2][64];
   extern __shared__ float sum_w[];          // [D] where several rows share a CTA
   wait_for_previous_grid();
@@ -412,7 +415,11 @@ add_norm_bwd_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* _
     float hv[NV][kRun], da[NV][kRun], ss = 0.f, ax = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) { hr[k].get(hv[k]); dr[k].get(da[k]); }
+    Raw<R, kRun> now[NV];                   // this row's dh
+#pragma unroll
+    for (int k = 0; k < NV; ++k) now[k] = gr[k];
     fetch_row(row + step);
+    if (kEarly) fetch_dh(row + step);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float wf[kRun];
@@ -429,7 +436,7 @@ add_norm_bwd_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* _
     for (int k = 0; k < NV; ++k) {
       float wf[kRun], gv[kRun];
       wv[k].get(wf);
-      gr[k].get(gv);
+      now[k].get(gv);
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
         dw[k][i] = fmaf(da[k][i], hv[k][i] * r1, dw[k][i]);
@@ -444,7 +451,7 @@ add_norm_bwd_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* _
         }
       }
     }
-    fetch_dh(row + step);
+    if (!kEarly) fetch_dh(row + step);
   }
   if (part == nullptr) return;
   allow_next_grid();
