@@ -264,14 +264,15 @@ template <bool ODD> struct Columns {
   __device__ __forceinline__ int at(int k) const { return (k * (int)blockDim.x + (int)threadIdx.x) * kRun - lead; }
   template <typename T> __device__ __forceinline__ void load(Raw<T, kRun>& r, const T* base, int64_t row, int c) const {
     const T* p = base + row * D + c;
-    if (c + kRun <= D && (!ODD || c >= 0)) {
-      r.load(p);
-    } else if (ODD && c < D && c > -kRun) {
-      if ((c >= 0 || row > 0) && (c + kRun <= D || row + 1 < rows)) { r.load(p); r.keep(-c, D - c); }
-      else r.load_part(p, -c, D - c);
-    } else {
-      r.zero();
-    }
+    const bool here = c < D && (!ODD || c > -kRun);
+    if (here && (!ODD || ((c >= 0 || row > 0) && (c + kRun <= D || row + 1 < rows)))) r.load(p);
+    else if (ODD && here) r.load_part(p, -c, D - c);
+    else r.zero();
+  }
+  // takes the neighbours' elements out of a loaded run: at its use, so that no load is waited for
+  // before
+  template <typename T> __device__ __forceinline__ void clip(Raw<T, kRun>& r, int c) const {
+    if (ODD && c < D && (c < 0 || c + kRun > D)) r.keep(-c, D - c);
   }
   // of a vector that begins at column 0, whatever the row's lead
   template <typename T> __device__ __forceinline__ void load_w(Raw<T, kRun>& r, const T* w, int c) const {
@@ -333,25 +334,37 @@ add_norm_kernel(const T* __restrict__ x, const R* res, const T* __restrict__ w, 
 #pragma unroll
     for (int k = 0; k < NV; ++k) cols.load_w(wv[k], w, cols.at(k));
   }
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  Raw<T, kRun> xr[NV];
+  Raw<R, kRun> rr[NV];
+  auto fetch = [&](int64_t r) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      xr[k].zero(); rr[k].zero();
+      if (r < rows) { cols.load(xr[k], x, r, cols.at(k)); cols.load(rr[k], res, r, cols.at(k)); }
+    }
+  };
+  fetch(row);
+  if (!ODD) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) cols.load_w(wv[k], w, cols.at(k));
+  }
   int turn = 0;
   do {
     const bool live = row < rows;
     float v[NV][kRun], ss = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      Raw<T, kRun> xr;
-      Raw<R, kRun> rr;
-      xr.zero(); rr.zero();
-      if (live) { cols.load(xr, x, row, cols.at(k)); cols.load(rr, res, row, cols.at(k)); }
-      if (!ODD) cols.load_w(wv[k], w, cols.at(k));
+      cols.clip(xr[k], cols.at(k)); cols.clip(rr[k], cols.at(k));
       float xv[kRun];
-      xr.get(xv); rr.get(v[k]);
+      xr[k].get(xv); rr[k].get(v[k]);
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
         v[k][i] = fmaf(scale, xv[i], v[k][i]);
         ss = fmaf(v[k][i], v[k][i], ss);
       }
     }
+    if (ODD) fetch(row + step);
     const float rstd = rsqrtf(row_sum(ss, 0.f, sm, turn++).x * (1.0f / D) + eps);
     if (live) {
 #pragma unroll
@@ -364,7 +377,7 @@ add_norm_kernel(const T* __restrict__ x, const R* res, const T* __restrict__ w, 
         cols.store(n, row, cols.at(k), v[k]);
       }
     }
-    row += (int64_t)gridDim.x * blockDim.y;
+    row += step;
   } while (ODD && row - threadIdx.y < rows);      // aligned rows have a CTA each
 }
 
@@ -414,7 +427,10 @@ add_norm_bwd_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* _
   for (int64_t r0 = row - threadIdx.y; r0 < rows; r0 += step, row += step, ++turn) {
     float hv[NV][kRun], da[NV][kRun], ss = 0.f, ax = 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) { hr[k].get(hv[k]); dr[k].get(da[k]); }
+    for (int k = 0; k < NV; ++k) {
+      cols.clip(hr[k], cols.at(k)); cols.clip(dr[k], cols.at(k));
+      hr[k].get(hv[k]); dr[k].get(da[k]);
+    }
     Raw<R, kRun> now[NV];                   // this row's dh
 #pragma unroll
     for (int k = 0; k < NV; ++k) now[k] = gr[k];
@@ -504,6 +520,7 @@ add_norm_bwd_long_kernel(const R* __restrict__ h, const T* __restrict__ w, const
       Raw<R, kRun> hr;
       Raw<T, kRun> dr, wr;
       cols.load(hr, h, row, cols.at(k)); cols.load(dr, dn, row, cols.at(k)); cols.load_w(wr, w, cols.at(k));
+      cols.clip(hr, cols.at(k)); cols.clip(dr, cols.at(k));
       float hv[kRun], da[kRun], wf[kRun];
       hr.get(hv); dr.get(da); wr.get(wf);
 #pragma unroll
@@ -522,6 +539,7 @@ add_norm_bwd_long_kernel(const R* __restrict__ h, const T* __restrict__ w, const
       cols.load(hr, h, row, c); cols.load(dr, dn, row, c); cols.load_w(wr, w, c);
       gr.zero();
       if (dh) cols.load(gr, dh, row, c);
+      cols.clip(hr, c); cols.clip(dr, c);
       float hv[kRun], da[kRun], wf[kRun], gv[kRun];
       hr.get(hv); dr.get(da); wr.get(wf); gr.get(gv);
       float* mw = sum_w + c + cols.lead;
@@ -571,7 +589,7 @@ template <typename T, typename R, int NV, int MAXT, bool ODD>
 cudaError_t add_fwd(const AddNorm& a, cudaStream_t st) {
   const AddShape s = add_shape(a.D, NV);
   // aligned rows: a CTA for each group of rows; odd ones: resident CTAs, which load w's parts once
-  const unsigned grid = grid_of((a.rows + s.ty - 1) / s.ty, ODD ? 148 * (2048 / MAXT) : 1LL << 31, ODD);
+  const unsigned grid = grid_of((a.rows + s.ty - 1) / s.ty, ODD ? 148 * (1024 / MAXT) : 1LL << 31, ODD);
   return launch_overlapped(add_norm_kernel<T, R, NV, MAXT, ODD>, dim3(grid), dim3(s.tx, s.ty), 0, st, (const T*)a.x,
                            (const R*)a.res, (const T*)a.w, a.scale, a.w_add, a.eps, (R*)a.h, (T*)a.n, a.rows, a.D);
 }
@@ -612,8 +630,8 @@ cudaError_t add_bwd_long(const AddNorm& a, cudaStream_t st) {
 // shuffles are paid by all of them), as many CTAs as fit. (Backward, 16,384 x 4,096, fp32 residual:
 // two runs by 256 threads 172 us, one run by 512 226; 8,000 x 8,192, bf16: forward by 512 threads 79
 // us, by 1,024 95; 4,000 x 16,384: backward reading the row twice 198 us, by registers that spill
-// 484. Odd rows: 5,000 x 7,001, bf16: forward 66 us and backward 132, element by element 204 and
-// 588; 20,000 x 1,001 40 and 60, element by element 45 and 80.)
+// 484. Odd rows: 5,000 x 7,001, bf16: forward 66 us and backward 77, element by element 204 and
+// 588; 20,000 x 1,001 31 and 50, element by element 45 and 80.)
 template <typename T, typename R, bool ODD>
 cudaError_t add_odd(const AddNorm& a, cudaStream_t st) {
   const int runs = runs_of(a.D);
