@@ -153,9 +153,11 @@ __device__ __forceinline__ void seq_bounds(const int32_t* cu, int32_t n, int64_t
   bos = a; eos = b;
 }
 
-// Asynchronous copies of 16 bytes, global to shared memory; a thread waits for its own groups.
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Asynchronous copies of 8 or 16 bytes, global to shared memory; a thread waits for its own groups.
+template <int BYTES> __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  static_assert(BYTES == 8 || BYTES == 16, "");
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }

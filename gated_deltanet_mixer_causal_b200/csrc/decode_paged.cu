@@ -62,8 +62,11 @@ template <typename T> __device__ __forceinline__ float silu_for(float z);
 template <> __device__ __forceinline__ float silu_for<bf16>(float z) { return silu(z); }
 template <> __device__ __forceinline__ float silu_for<float>(float z) { return z / (1.0f + expf(-z)); }
 
-// a * b + c. With fp32 activations every operation is rounded on its own, as the definition's
-// elementary operations are: states stored in bf16 then round the same way almost everywhere.
+// a * b + c. With fp32 activations every operation of the state's way is rounded on its own, as the
+// definition's elementary operations are, and its sums are added in the order in which a warp adds
+// up a row: states then equal those of a form put together from elementary tensor operations, and,
+// stored in bf16, round the same way (by fused operations about 1 in 10^4 went the other way, and
+// the outputs of the next call with them by 3e-5). The path is bound by HBM all the same.
 template <typename T> __device__ __forceinline__ float mul_add(float a, float b, float c);
 template <> __device__ __forceinline__ float mul_add<bf16>(float a, float b, float c) { return fmaf(a, b, c); }
 template <> __device__ __forceinline__ float mul_add<float>(float a, float b, float c) { return __fadd_rn(__fmul_rn(a, b), c); }
@@ -90,14 +93,12 @@ __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+// a + b c with the product rounded before it is added, which the paired instructions, put together
+// by the assembler, would not be
+__device__ __forceinline__ f2 add_product(f2 a, f2 b, f2 c) {
+  const float2 x = unpair(a), y = unpair(b), z = unpair(c);
+  return pair(__fadd_rn(x.x, __fmul_rn(y.x, z.x)), __fadd_rn(x.y, __fmul_rn(y.y, z.y)));
 }
-template <typename T> __device__ __forceinline__ f2 mul_add2(f2 a, f2 b, f2 c);
-template <> __device__ __forceinline__ f2 mul_add2<bf16>(f2 a, f2 b, f2 c) { return fma2(a, b, c); }
-template <> __device__ __forceinline__ f2 mul_add2<float>(f2 a, f2 b, f2 c) { return add2(mul2(a, b), c); }
 
 // Eight channels as they lie in memory.
 template <typename T> struct Raw8 {
@@ -124,10 +125,11 @@ template <typename T> struct Raw8 {
   }
 };
 
-// 16 bytes of a state row as pairs, and back (rounded to nearest even once for bf16).
-template <typename S> struct Chunk;
-template <> struct Chunk<float> {
-  static constexpr int kPairs = 2;
+// N consecutive elements of a state row (a word of 8 or 16 bytes) as pairs, and back (rounded to
+// nearest even once for bf16).
+template <typename S, int N> struct Chunk;
+template <> struct Chunk<float, 4> {
+  typedef uint4 Word;
   static __device__ __forceinline__ void get(uint4 u, f2* p) {
     p[0] = pair(__uint_as_float(u.x), __uint_as_float(u.y));
     p[1] = pair(__uint_as_float(u.z), __uint_as_float(u.w));
@@ -137,23 +139,25 @@ template <> struct Chunk<float> {
     return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
   }
 };
-template <> struct Chunk<bf16> {
-  static constexpr int kPairs = 4;
+__device__ __forceinline__ f2 widen(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+__device__ __forceinline__ uint32_t narrow(f2 p) {
+  const float2 f = unpair(p);
+  __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+template <> struct Chunk<bf16, 8> {
+  typedef uint4 Word;
   static __device__ __forceinline__ void get(uint4 u, f2* p) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    p[0] = widen(u.x); p[1] = widen(u.y); p[2] = widen(u.z); p[3] = widen(u.w);
   }
   static __device__ __forceinline__ uint4 put(const f2* p) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpair(p[i]);
-      __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
-      w[i] = *reinterpret_cast<uint32_t*>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(narrow(p[0]), narrow(p[1]), narrow(p[2]), narrow(p[3]));
   }
+};
+template <> struct Chunk<bf16, 4> {
+  typedef uint2 Word;
+  static __device__ __forceinline__ void get(uint2 u, f2* p) { p[0] = widen(u.x); p[1] = widen(u.y); }
+  static __device__ __forceinline__ uint2 put(const f2* p) { return make_uint2(narrow(p[0]), narrow(p[1])); }
 };
 
 // What the row loop needs of a token and value head. The state is carried as gamma times the
@@ -199,8 +203,11 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
   constexpr int L = D / kSeg;              // lanes per state row
   constexpr int RPW = 32 / L;              // rows a warp covers at once
   constexpr int RPP = RPW * kRows;         // rows of a warp's pass
-  constexpr int CE = 16 / sizeof(S);       // elements of a 16-byte chunk
+  constexpr bool kPlain = sizeof(T) == 4;  // fp32 activations: the definition's own operations (see mul_add)
+  constexpr int CE = kPlain ? 4 : 16 / sizeof(S);      // elements of a lane's chunk
   constexpr int CH = kSeg / CE;            // chunks of a lane's row part
+  typedef Chunk<S, CE> Part;
+  typedef typename Part::Word Word;
   constexpr int NST = kStages<S>;
   const int G1 = a.Hv / a.Hk, G = KH * G1, W = KH * D, n_tok = a.n_tok;
   const int32_t Cc = 2 * a.Hk * D + a.Hv * D;
@@ -238,7 +245,7 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
   const bool fresh = rp < 0 || rp >= a.n_pages;
 
   extern __shared__ __align__(16) char smem_raw[];
-  uint4* ring = reinterpret_cast<uint4*>(smem_raw) + warp * (NST * kRows * CH * 32) + lane;   // [stage][row][chunk][lane]
+  Word* ring = reinterpret_cast<Word*>(smem_raw) + warp * (NST * kRows * CH * 32) + lane;     // [stage][row][chunk][lane]
   Step* steps = reinterpret_cast<Step*>(smem_raw + kWarps * NST * kPass * sizeof(S));         // [n_tok][G]
   float* qk = reinterpret_cast<float*>(steps + n_tok * G);      // [n_tok][KH][2 D] q | k
   float* vo = qk + n_tok * 2 * W;          // [n_tok][rows] v, then o in its place
@@ -268,7 +275,8 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
         if (r < w.end) {
 #pragma unroll
           for (int j = 0; j < CH; ++j)
-            copy_async(ring_at + ((stage * kRows + i) * CH + j) * 512, src + (int64_t)r * D + j * CE * L);
+            copy_async<sizeof(Word)>(ring_at + ((stage * kRows + i) * CH + j) * (32 * sizeof(Word)),
+                                     src + (int64_t)r * D + j * CE * L);
         }
       }
     }
@@ -279,6 +287,9 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
 
   // 1. conv + SiLU over this CTA's channels, eight a thread; the window slides in registers. q and
   //    k are laid out as the lanes of a row read them: quad i of a lane at 4 L i + 4 seg.
+  const auto place = [](int c) {           // of column c in a vector of q or k
+    return (c / (CE * L) * CE + c % CE) / 4 * (4 * L) + c % (CE * L) / CE * 4 + c % 4;
+  };
   T* conv = static_cast<T*>(a.conv_pool);
   Raw8<T> w0, w1, w2;
   auto fetch_taps = [&]() {
@@ -313,8 +324,8 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
     const bool keeps = rank == 0 || lc >= 2 * W;
     const auto quad_at = [&](int c) {      // where four channels of q or k, or v, begin in shared memory
       if (c >= 2 * W) return (int)(vo - qk) + c - 2 * W;
-      const int h = c < W ? 0 : D, cw = c < W ? c : c - W, cc = cw % D;
-      return cw / D * (2 * D) + h + (cc / (CE * L) * CE + cc % CE) / 4 * (4 * L) + cc % (CE * L) / CE * 4;
+      const int h = c < W ? 0 : D, cw = c < W ? c : c - W;
+      return cw / D * (2 * D) + h + place(cw % D);
     };
     const int at_a = quad_at(lc), at_b = quad_at(lc + 4), at_step = lc < 2 * W ? 2 * W : rows;
     for (int t0 = 0; t0 < nv; t0 += kAhead) {
@@ -352,17 +363,19 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
     float* yt = qk + e * 2 * D;
     const bool active = lane * VEC < D;
     float qv[VEC], kv[VEC], qq = 0.f, kk = 0.f, kq = 0.f;
+    int at[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      qv[j] = active ? yt[lane * VEC + j] : 0.f;
-      kv[j] = active ? yt[D + lane * VEC + j] : 0.f;
-      qq = fmaf(qv[j], qv[j], qq); kk = fmaf(kv[j], kv[j], kk); kq = fmaf(kv[j], qv[j], kq);
+      at[j] = place((D == 128 ? lane * VEC + j : lane + 32 * j) % D);
+      qv[j] = active ? yt[at[j]] : 0.f;
+      kv[j] = active ? yt[D + at[j]] : 0.f;
+      qq = mul_add<T>(qv[j], qv[j], qq); kk = mul_add<T>(kv[j], kv[j], kk); kq = fmaf(kv[j], qv[j], kq);
     }
     qq = warp_sum(qq); kk = warp_sum(kk); kq = warp_sum(kq);
     const float nq = sqrtf(qq + kEps), nk = sqrtf(kk + kEps);
     if (active) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) { yt[lane * VEC + j] = qv[j] / nq; yt[D + lane * VEC + j] = kv[j] / nk; }
+      for (int j = 0; j < VEC; ++j) { yt[at[j]] = qv[j] / nq; yt[D + at[j]] = kv[j] / nk; }
     }
     if (lane == 0) kqs[e] = kq / (nq * nk);
   }
@@ -395,9 +408,9 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
     for (int i = 0; i < kRows; ++i)
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        uint4 u = make_uint4(0, 0, 0, 0);
+        Word u = {};
         if (!fresh && ra + i * RPW < end) u = ring[((stage * kRows + i) * CH + j) * 32];
-        Chunk<S>::get(u, &s[i][j * Chunk<S>::kPairs]);
+        Part::get(u, &s[i][j * CE / 2]);
       }
     fetch(pass + NST * kWarps, stage);
     stage = stage + 1 == NST ? 0 : stage + 1;
@@ -411,6 +424,46 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
       constexpr int NR = kRows > L ? kRows / L : 1, SAME = L > kRows ? L / kRows : 1;
       const int r0 = seg * kRows / L;
       float sk[kRows], sq[kRows];
+      // fp32 activations: the state decays first, and its products with k are rounded and added up one
+      // by one, in the order of a sum over lanes of a warp (fours of neighbours at 128 columns, then
+      // halves)
+      auto plain_dots = [&](const float* vec, float (&sums)[kRows]) {
+        float tot[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          float q[4][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const ulonglong2 v4 = *reinterpret_cast<const ulonglong2*>(vec + j * 4 * L);
+            const float2 lo = unpair(mul2(s[i][2 * j], v4.x)), hi = unpair(mul2(s[i][2 * j + 1], v4.y));
+            q[j][0] = lo.x; q[j][1] = lo.y; q[j][2] = hi.x; q[j][3] = hi.y;
+          }
+          if constexpr (D == 128) {
+            float f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              f[j] = __fadd_rn(__fadd_rn(__fadd_rn(q[j][0], q[j][1]), q[j][2]), q[j][3]);
+            tot[i] = __fadd_rn(__fadd_rn(f[0], f[2]), __fadd_rn(f[1], f[3]));
+#pragma unroll
+            for (int m = L / 2; m >= 1; m >>= 1) tot[i] += __shfl_xor_sync(0xffffffffu, tot[i], m);
+          } else {
+            float f[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              f[x] = __fadd_rn(__fadd_rn(q[0][x], q[2][x]), __fadd_rn(q[1][x], q[3][x]));
+#pragma unroll
+              for (int m = L / 2; m >= 1; m >>= 1) f[x] += __shfl_xor_sync(0xffffffffu, f[x], m);
+            }
+            tot[i] = __fadd_rn(__fadd_rn(f[0], f[2]), __fadd_rn(f[1], f[3]));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {       // this lane's rows, as scatter_sums leaves them
+          sums[i] = tot[0];
+#pragma unroll
+          for (int c = 1; c < kRows; ++c) sums[i] = r0 + i == c ? tot[c] : sums[i];
+        }
+      };
       auto dots = [&](const float* vec, float (&sums)[kRows]) {
         f2 acc[kRows];
 #pragma unroll
@@ -431,7 +484,19 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
         }
         scatter_sums<L, kRows>(sums, seg);
       };
-      dots(qt + D, sk);
+      if constexpr (kPlain) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int r = ra + i * RPW;
+          const float alpha = r < end ? st[(row0 + r) / D].gamma : 0.f;
+          const f2 aa = pair(alpha, alpha);
+#pragma unroll
+          for (int j = 0; j < kSeg / 2; ++j) s[i][j] = mul2(aa, s[i][j]);
+        }
+        plain_dots(qt + D, sk);
+      } else {
+        dots(qt + D, sk);
+      }
       dots(qt, sq);
       float u[NR], gam[kRows], inv[kRows];
       if constexpr (RPP <= D) {             // a pass lies in one head
@@ -441,7 +506,7 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
           const int r = ra + (r0 + i) * RPW;
-          u[i] = p.y * ((r < end ? vt[r] : 0.f) - p.x * sk[i]);
+          u[i] = p.y * ((r < end ? vt[r] : 0.f) - (kPlain ? sk[i] : p.x * sk[i]));
         }
       } else {
 #pragma unroll
@@ -453,7 +518,7 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
           const int r = ra + (r0 + i) * RPW, rr = r < end ? r : 0;
-          u[i] = st[(row0 + rr) / D].beta * (vt[rr] - st[(row0 + rr) / D].gamma * sk[i]);
+          u[i] = st[(row0 + rr) / D].beta * (vt[rr] - (kPlain ? sk[i] : st[(row0 + rr) / D].gamma * sk[i]));
         }
       }
       f2 uu[kRows];
@@ -470,7 +535,7 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
           const int r = ra + (r0 + i) * RPW;
           if (r < end) {
             const float gm = RPP <= D ? gam[0] : st[(row0 + r) / D].gamma;
-            vt[r] = a.scale * fmaf(gm, sq[i], u[i] * kq);
+            vt[r] = a.scale * fmaf(kPlain ? 1.f : gm, sq[i], u[i] * kq);
           }
         }
       }
@@ -494,8 +559,8 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
 #pragma unroll
           for (int i = 0; i < kRows; ++i) {
             const f2 aa = pair(gam[i], gam[i]);
-            s[i][2 * j] = mul_add2<T>(aa, s[i][2 * j], mul2(uu[i], k4.x));
-            s[i][2 * j + 1] = mul_add2<T>(aa, s[i][2 * j + 1], mul2(uu[i], k4.y));
+            s[i][2 * j] = kPlain ? add_product(s[i][2 * j], uu[i], k4.x) : fma2(aa, s[i][2 * j], mul2(uu[i], k4.x));
+            s[i][2 * j + 1] = kPlain ? add_product(s[i][2 * j + 1], uu[i], k4.y) : fma2(aa, s[i][2 * j + 1], mul2(uu[i], k4.y));
           }
         }
         const int32_t to = wp[t];
@@ -506,7 +571,7 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
             if (ra + i * RPW < end) {
 #pragma unroll
               for (int j = 0; j < CH; ++j)
-                __stcs(reinterpret_cast<uint4*>(dst + i * RPW * D + j * CE * L), Chunk<S>::put(&s[i][j * Chunk<S>::kPairs]));
+                __stcs(reinterpret_cast<Word*>(dst + i * RPW * D + j * CE * L), Part::put(&s[i][j * CE / 2]));
             }
         }
       }
