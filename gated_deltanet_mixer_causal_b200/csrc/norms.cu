@@ -250,7 +250,7 @@ norm_dw_kernel(const float* __restrict__ part, int n_part, int D, float* __restr
 // blockDim = (threads a row, rows a CTA); a thread holds NV runs of 8 elements of its row. All
 // tensors of rows lie alike, so a run that is aligned in one is aligned in all. Where D is not a
 // multiple of 8 (ODD) a row begins `lead` elements behind a run's boundary: its first and last run
-// are partly the neighbours'. They are read whole, but for the first and the last of the tensor, and
+// are partly the neighbours'. They are read whole, but for one that passes the tensor's end, and
 // written element by element. A thread's rows are a multiple of 8 apart, so that `lead`, and with it
 // the thread's columns of w and dw, stays the same.
 
@@ -263,9 +263,10 @@ template <bool ODD> struct Columns {
       : lead(ODD ? (int)((row * D_) & (kRun - 1)) : 0), D(D_), rows(rows_) {}
   __device__ __forceinline__ int at(int k) const { return (k * (int)blockDim.x + (int)threadIdx.x) * kRun - lead; }
   template <typename T> __device__ __forceinline__ void load(Raw<T, kRun>& r, const T* base, int64_t row, int c) const {
-    const T* p = base + row * D + c;
+    const int64_t at = row * D + c;        // a multiple of a run, so never below 0
+    const T* p = base + at;
     const bool here = c < D && (!ODD || c > -kRun);
-    if (here && (!ODD || ((c >= 0 || row > 0) && (c + kRun <= D || row + 1 < rows)))) r.load(p);
+    if (here && (!ODD || at + kRun <= rows * D)) r.load(p);
     else if (ODD && here) r.load_part(p, -c, D - c);
     else r.zero();
   }

@@ -167,6 +167,29 @@ def test_add_norm_keeps_to_its_rows(cuda_device, T, D):
         assert torch.isnan(buf[t.numel():]).all()
 
 
+@pytest.mark.parametrize("D", range(1, 8))
+@pytest.mark.parametrize("dt,res", [(BF, FP), (FP, BF)])
+def test_add_norm_of_rows_shorter_than_a_run(cuda_device, D, dt, res):
+    """Several rows lie in one run of eight elements, and the last runs pass the end of the tensor,
+    which lies at the end of its buffer."""
+    for T in (1, 2, 7, 9, 16, 1201):
+        ts = add_case(T, D, dt, res, T + D)
+        x, r, w, dn, dh = (t.to(cuda_device) for t in ts)
+        h64 = R.f64(r) + R.f64(x)
+        size = R.f64(r).abs() + R.f64(x).abs()
+        rms = (h64.square().mean(-1, keepdim=True) + 1e-6) ** -0.5
+        n, h = gdn.gdn_add_norm(x, r, w)
+        name, k = f"add {dt} {T}x{D}", 160 * R.U
+        n64 = h64 * rms * R.f64(w)
+        check(name, "h", R.worst(h, h64, h64.abs() * R.HALF[res] + size * 2 * R.U + 1e-30), 1.0)
+        check(name, "n", R.worst(n, n64, n64.abs() * R.HALF[dt] + size * rms * R.f64(w).abs() * k + 1e-30), 1.0)
+        ref = add_terms(h, w, dn, dh, 1.0, 0.0, 1e-6)
+        dx, dres, dw = gdn.gdn_add_norm_bwd(h, w, dn, dh)
+        check(name, "dres", R.worst(dres, ref["dres"], ref["dres"].abs() * R.HALF[res] + ref["dres_abs"] * k + 1e-30), 1.0)
+        check(name, "dx", R.worst(dx, ref["dx"], ref["dx"].abs() * R.HALF[dt] + ref["dres_abs"] * k + 1e-30), 1.0)
+        check(name, "dw", R.worst(dw, ref["dw"], ref["dw_abs"] * (T / 592 + 200) * R.U + 1e-30), 1.0)
+
+
 def test_gradients_against_differences(cuda_device):
     """Directional derivatives by central differences of the fp64 forward formulas: with a step
     of 1e-5 they are exact to about 1e-9, so the kernels' fp32 error (counted above, summed over
