@@ -130,7 +130,7 @@ gated_norm_kernel(const T* o, const T* __restrict__ z, int64_t z_stride, const T
     if (r < rows) {
       const uint2 th = div_rows(r, H, magic);
       ov[u].load(o + (int64_t)r * D + col);
-      zv[u].load(z + (int64_t)th.x * z_stride + th.y * D + col);
+      zv[u].load(z + (int64_t)th.x * z_stride + (int64_t)th.y * D + col);
     }
   }
   wv.load(w + col);
@@ -174,7 +174,7 @@ gated_norm_bwd_kernel(const T* __restrict__ o, const T* __restrict__ z, int64_t 
       th[u] = div_rows(r, H, magic);
       if (r < rows) {
         ov[u].load(o + (int64_t)r * D + col);
-        zv[u].load(z + (int64_t)th[u].x * z_stride + th[u].y * D + col);
+        zv[u].load(z + (int64_t)th[u].x * z_stride + (int64_t)th[u].y * D + col);
         dv[u].load(dy + (int64_t)r * D + col);
       }
     }
@@ -203,7 +203,7 @@ gated_norm_bwd_kernel(const T* __restrict__ o, const T* __restrict__ z, int64_t 
       }
       if (r < rows) {
         VecIO<T, VEC>::store(dout + (int64_t)r * D + col, da);
-        VecIO<T, VEC>::store(dz + (int64_t)th[u].x * dz_stride + th[u].y * D + col, gz);
+        VecIO<T, VEC>::store(dz + (int64_t)th[u].x * dz_stride + (int64_t)th[u].y * D + col, gz);
       }
     }
   }
