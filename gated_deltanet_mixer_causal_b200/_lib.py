@@ -425,6 +425,14 @@ def _dense_from(t: torch.Tensor, name: str, dim: int, what: str) -> int:
     return inner
 
 
+def _apart(t: torch.Tensor, name: str, stride: int, row: int, what: str) -> int:
+    """``stride``, which must cover a row: what an expanded tensor repeats has no rows of its own,
+    and its stride of 0 would stand for a dense one."""
+    if stride < row:
+        raise ValueError(f"{name}: {what} must not share memory (expanded or overlapping), got strides {t.stride()}")
+    return stride
+
+
 def _token_rows(t: torch.Tensor, name: str, lead: int) -> int:
     """The token stride of t, whose first ``lead`` (1 or 2) dimensions count tokens that follow
     one another at one stride; the dimensions behind them must be dense. 0 stands for a dense t."""
@@ -433,12 +441,12 @@ def _token_rows(t: torch.Tensor, name: str, lead: int) -> int:
     inner = _dense_from(t, name, lead, "the dimensions behind the tokens")
     shape, strides = t.shape, t.stride()
     if lead == 1:
-        return inner if shape[0] <= 1 else strides[0]
+        return inner if shape[0] <= 1 else _apart(t, name, strides[0], inner, "tokens")
     if shape[1] <= 1:
-        return inner if shape[0] <= 1 else strides[0]
+        return inner if shape[0] <= 1 else _apart(t, name, strides[0], inner, "tokens")
     if shape[0] > 1 and strides[0] != strides[1] * shape[1]:
         raise ValueError(f"{name}: tokens must follow one another at one stride, got strides {strides}")
-    return strides[1]
+    return _apart(t, name, strides[1], inner, "tokens")
 
 
 def _page_stride(t: torch.Tensor, name: str) -> int:
@@ -446,7 +454,7 @@ def _page_stride(t: torch.Tensor, name: str) -> int:
     if t.is_contiguous():
         return 0
     page = _dense_from(t, name, 1, "pages")
-    return page if t.shape[0] <= 1 else t.stride(0)
+    return page if t.shape[0] <= 1 else _apart(t, name, t.stride(0), page, "pages")
 
 
 def gdn_decode_paged(x: torch.Tensor, conv_w: torch.Tensor, conv_pool: torch.Tensor, state_pool: torch.Tensor,
@@ -458,7 +466,7 @@ def gdn_decode_paged(x: torch.Tensor, conv_w: torch.Tensor, conv_pool: torch.Ten
     ``conv_pool`` [P, 3, Cc] and ``state_pool`` [P, Hv, dv, dk] (fp32 or bf16 storage): sequence b
     starts from page ``read_pages[b]`` (-1: from zeros); the state after its token t goes to page
     ``write_pages[b, t]`` (-1: nowhere), or without ``write_pages`` the last one back to the page
-    it read. x [B, n_tok, Cc] (tokens may be strided), g, beta [B, n_tok, Hv]. ``n_valid`` [B]
+    it read. x [B, n_tok, Cc] (tokens may be strided, not expanded), g, beta [B, n_tok, Hv]. ``n_valid`` [B]
     limits each sequence's tokens; rows of ``o`` behind them stay as they were (in an ``o`` made
     here they are not defined). With the gate ``z`` [B, n_tok, Hv, dv] and ``norm_w`` [dv] the
     output is gated and normalised as by ``gdn_gated_norm``. A page that one sequence writes must
@@ -512,6 +520,10 @@ def _pool_layout(t: torch.Tensor, name: str, page_dim: int):
         page = strides[page_dim] * es
     else:
         page = _dense_from(t, name, page_dim + 1, "pages") * es
+        if pages > 1:
+            _apart(t, name, strides[page_dim] * es, page, "pages")
+        if layers > 1:
+            _apart(t, name, strides[0] * es, page, "layers")
     return pages, layers, page, strides[page_dim] * es if pages > 1 else page, strides[0] * es if layers > 1 else 0
 
 
@@ -664,7 +676,7 @@ def _norm_workspace(D: int, workspace: Optional[torch.Tensor], device):
 def gdn_gated_norm(o: torch.Tensor, z: torch.Tensor, w: torch.Tensor, eps: float = 1e-6,
                    y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """o / sqrt(mean(o^2) + eps) * w * SiLU(z) over the last dimension: o [T, Hv, dv], z the same
-    (tokens may be strided), w [dv]. ``y`` may be ``o``."""
+    (tokens may be strided, not expanded), w [dv]. ``y`` may be ``o``."""
     dev, dt, shape = _device_of(o, "o"), o.dtype, o.shape
     T, Hv, dv = shape
     _want(o, "o", shape, dt, dev)
