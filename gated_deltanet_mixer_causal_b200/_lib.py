@@ -200,6 +200,8 @@ def _row_view(t: torch.Tensor, name: str):
     if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
         raise ValueError(f"{name} must be [T, H, d] with dense heads (strides (*, d, 1)), "
                          f"got strides {t.stride()}")
+    if t.shape[0] > 1 and t.stride(0) == 0:      # 0 stands for a dense tensor in the C ABI
+        raise ValueError(f"{name}: tokens must not share memory (expanded), got strides {t.stride()}")
     return t.stride(0)
 
 

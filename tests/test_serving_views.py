@@ -32,6 +32,13 @@ def test_tokens_that_share_memory_are_refused(t, lead):
         _lib._token_rows(t, "x", lead)
 
 
+def test_prefill_tokens_that_share_memory_are_refused():
+    one = torch.zeros(1, 2, 16)
+    with pytest.raises(ValueError, match="share memory"):
+        _lib._row_view(one.expand(9, 2, 16), "q")
+    assert _lib._row_view(one, "q") == 32 and _lib._row_view(torch.zeros(4, 64)[:, :32].unflatten(1, (2, 16)), "q") == 64
+
+
 def test_pages_that_share_memory_are_refused():
     pool = torch.zeros(1, 2, 16)
     for t in (pool.expand(5, 2, 16), torch.zeros(99).as_strided((5, 2, 8), (8, 8, 1))):
