@@ -194,7 +194,8 @@ gated_norm_bwd_kernel(const T* __restrict__ o, const T* __restrict__ z, int64_t 
         ax = fmaf(da[i], x[i], ax);
       }
       ss = lanes_sum<LANES>(ss); ax = lanes_sum<LANES>(ax);
-      const float r1 = rsqrtf(ss * (1.0f / D) + eps), c = ax * r1 * r1 * (1.0f / D);
+      // 0 behind the last row, whose zeros would give dw inf * 0 with eps = 0
+      const float r1 = r < rows ? rsqrtf(ss * (1.0f / D) + eps) : 0.f, c = ax * r1 * r1 * (1.0f / D);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         dw[i] = fmaf(d[i], x[i] * r1, dw[i]);
@@ -448,7 +449,8 @@ add_norm_bwd_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* _
       }
     }
     const float2 s = row_sum(ss, ax, sm, turn);
-    const float r1 = rsqrtf(fmaf(s.x, inv_d, eps)), cc = -s.y * r1 * r1 * inv_d;
+    // 0 behind the last row, whose zeros would give dw inf * 0 with eps = 0
+    const float r1 = row < rows ? rsqrtf(fmaf(s.x, inv_d, eps)) : 0.f, cc = -s.y * r1 * r1 * inv_d;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float wf[kRun], gv[kRun];

@@ -5,6 +5,9 @@ import pytest
 import torch
 
 import gated_deltanet_mixer_causal_b200 as gdn
+import serving_ref as R
+from parity import check
+from test_gpu_norms import add_case, add_terms, gated_case, gated_terms, slack
 from test_gpu_paged import case, ints
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +43,30 @@ def test_expanded_tensors_are_refused(cuda_device):
         with pytest.raises(ValueError, match="share memory"):
             call()
     assert (pool == 0).all() and refs.tolist() == [1, 0, 0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("T,H,d", [(1, 1, 128), (7, 5, 128), (33, 5, 64), (9, 3, 16), (601, 5, 32)])
+def test_gated_norm_without_eps(cuda_device, dt, T, H, d):
+    """eps = 0 with no row of zeros: the rows that fill up the last group add nothing to dw."""
+    o, z, w, dy = gated_case(T, H, d, dt, T + H, False)
+    ref = gated_terms(o, z, w, dy, 0.0)
+    do, dz, dw = gdn.gdn_gated_norm_bwd(*(t.to(cuda_device) for t in (o, z, w, dy)), eps=0.0)
+    y = gdn.gdn_gated_norm(*(t.to(cuda_device) for t in (o, z, w)), eps=0.0)
+    name, c, fast = f"gated eps 0 {dt} {T}x{H}x{d}", 160 * R.U + 2 * slack(dt), slack(dt)
+    check(name, "y", R.worst(y, ref["y"], ref["y"].abs() * (R.HALF[dt] + 100 * R.U + fast) + 1e-30), 1.0)
+    check(name, "do", R.worst(do, ref["do"], ref["do"].abs() * R.HALF[dt] + ref["do_abs"] * c + 1e-30), 1.0)
+    check(name, "dz", R.worst(dz, ref["dz"], ref["dz"].abs() * R.HALF[dt] + ref["dz_abs"] * c + 1e-30), 1.0)
+    check(name, "dw", R.worst(dw, ref["dw"], ref["dw_abs"] * ((T * H / 592 + 200) * R.U + 2 * fast) + 1e-30), 1.0)
+
+
+@pytest.mark.parametrize("dt,res", [(BF, BF), (BF, FP), (FP, FP)])
+@pytest.mark.parametrize("T,D", [(1, 64), (3, 1024), (5, 16), (7, 1001), (601, 200), (3, 7), (3, 9), (2, 16384)])
+def test_add_norm_without_eps(cuda_device, dt, res, T, D):
+    x, r, w, dn, dh = add_case(T, D, dt, res, T + D)
+    ref = add_terms(r, w, dn, dh, 1.0, 0.0, 0.0)
+    dx, dres, dw = gdn.gdn_add_norm_bwd(*(t.to(cuda_device) for t in (r, w, dn, dh)), eps=0.0)
+    name, k = f"add eps 0 {dt} {res} {T}x{D}", 160 * R.U
+    check(name, "dres", R.worst(dres, ref["dres"], ref["dres"].abs() * R.HALF[res] + ref["dres_abs"] * k + 1e-30), 1.0)
+    check(name, "dx", R.worst(dx, ref["dx"], ref["dx"].abs() * R.HALF[dt] + ref["dres_abs"] * k + 1e-30), 1.0)
+    check(name, "dw", R.worst(dw, ref["dw"], ref["dw_abs"] * (T / 592 + 200) * R.U + 1e-30), 1.0)
