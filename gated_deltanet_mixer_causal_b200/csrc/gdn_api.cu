@@ -47,11 +47,50 @@ bool pages_apart(int32_t pages, int64_t page, int32_t layers, int64_t layer, int
   return layer >= (pages - 1) * page + bytes || page >= (layers - 1) * layer + bytes || pages == 1;
 }
 
+int64_t greatest_common(int64_t a, int64_t b) {
+  while (b != 0) { const int64_t r = a % b; a = b; b = r; }
+  return a;
+}
+
 // [a, a + na) and [b, b + nb) share a byte (null or empty ranges never overlap).
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
   return x < y + nb && y < x + na;
+}
+
+// The pages of a pool in one layout: `bytes` at `at` + l * layer + p * page.
+struct Pages {
+  const void* at;
+  int64_t bytes, page, layer;
+  int32_t pages, layers;
+  size_t extent() const {
+    return pages > 0 && layers > 0 ? (size_t)((layers - 1) * layer + (pages - 1) * page + bytes) : 0;
+  }
+};
+
+// No page of one shares a byte with a page of the other: their extents lie apart, or both repeat at
+// a common step in which their parts do. The parts are single pages, or all the layers of a page
+// (records of a page), or all the pages of a layer.
+bool pools_apart(const Pages& a, const Pages& b) {
+  if (!overlap(a.at, a.extent(), b.at, b.extent())) return true;
+  const int64_t delta = (int64_t)((intptr_t)b.at - (intptr_t)a.at);
+  for (int part = 0; part < 3; ++part) {
+    int64_t step = 0, size[2];
+    const Pages* both[2] = {&a, &b};
+    for (int i = 0; i < 2; ++i) {
+      const Pages& p = *both[i];
+      size[i] = p.bytes;
+      if (part == 1) size[i] += (p.layers - 1) * p.layer;
+      else if (p.layers > 1) step = greatest_common(step, p.layer);
+      if (part == 2) size[i] += (p.pages - 1) * p.page;
+      else if (p.pages > 1) step = greatest_common(step, p.page);
+    }
+    if (step == 0) continue;
+    const int64_t from = (delta % step + step) % step;      // of b's part in the step that begins with a's
+    if (from >= size[0] && from + size[1] <= step) return true;
+  }
+  return false;
 }
 
 size_t elt_size(gdn_dtype_t dt) { return dt == GDN_F32 ? 4 : 2; }
@@ -456,7 +495,7 @@ gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32
     return fail(GDN_ERR_UNSUPPORTED, "pages_copy: %d entries, at most %d a call", n, gdn::kPagesMaxList);
   gdn::PagesCopy a{};
   a.src_pages = src_pages; a.dst_pages = dst_pages; a.src = src; a.dst = dst; a.n = n;
-  size_t db[gdn::kPagesMaxPools] = {}, sb[gdn::kPagesMaxPools] = {};
+  Pages from[gdn::kPagesMaxPools] = {}, to[gdn::kPagesMaxPools] = {};
   for (int i = 0; i < n_pools; ++i) {
     gdn_page_pool_t p = pools[i];
     if (p.page_bytes <= 0 || p.page_bytes % 16)
@@ -472,18 +511,17 @@ gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32
       return fail(GDN_ERR_INVALID_ARG, "pages_copy: pools and lists must be non-null");
     if (!aligned16(p.src) || !aligned16(p.dst) || !aligned4(src) || !aligned4(dst))
       return fail(GDN_ERR_INVALID_ARG, "pages_copy: pools must be 16-byte aligned, lists 4-byte aligned");
-    sb[i] = (size_t)((p.layers - 1) * p.src_layer_stride + (src_pages - 1) * p.src_page_stride + p.page_bytes);
-    db[i] = (size_t)((p.layers - 1) * p.dst_layer_stride + (dst_pages - 1) * p.dst_page_stride + p.page_bytes);
+    from[i] = {p.src, p.page_bytes, p.src_page_stride, p.src_layer_stride, src_pages, p.layers};
+    to[i] = {p.dst, p.page_bytes, p.dst_page_stride, p.dst_layer_stride, dst_pages, p.layers};
     const bool same = p.src == p.dst;
     if (same && (src_pages != dst_pages || p.src_page_stride != p.dst_page_stride ||
                  (p.layers > 1 && p.src_layer_stride != p.dst_layer_stride)))
       return fail(GDN_ERR_INVALID_ARG, "pages_copy: one pool, but different strides or page counts");
-    if (!same && overlap(p.src, sb[i], p.dst, db[i])) return fail(GDN_ERR_INVALID_ARG, "pages_copy: the pools overlap");
-    if (overlap(src, (size_t)n * 4, p.dst, db[i]) || overlap(dst, (size_t)n * 4, p.dst, db[i]))
+    if (!same && !pools_apart(from[i], to[i])) return fail(GDN_ERR_INVALID_ARG, "pages_copy: the pools overlap");
+    if (overlap(src, (size_t)n * 4, p.dst, to[i].extent()) || overlap(dst, (size_t)n * 4, p.dst, to[i].extent()))
       return fail(GDN_ERR_INVALID_ARG, "pages_copy: a list overlaps a destination pool");
     for (int j = 0; j < i; ++j)
-      if (overlap(p.dst, db[i], pools[j].dst, db[j]) || overlap(p.dst, db[i], pools[j].src, sb[j]) ||
-          overlap(p.src, sb[i], pools[j].dst, db[j]))
+      if (!pools_apart(to[i], to[j]) || !pools_apart(to[i], from[j]) || !pools_apart(from[i], to[j]))
         return fail(GDN_ERR_INVALID_ARG, "pages_copy: the pools overlap");
     a.pool[a.n_pools++] = {(const char*)p.src, (char*)p.dst, p.page_bytes, p.src_page_stride, p.src_layer_stride,
                            p.dst_page_stride, p.dst_layer_stride, p.layers, same};

@@ -397,7 +397,9 @@ gdn_status_t gdn_decode_paged(const void* x, int64_t x_stride, const void* conv_
  *              page_stride 0 means page_bytes). Pages hold any type; page_bytes is a positive
  *              multiple of 16. The pages of a pool must not overlap one another; src and dst are
  *              either the same pool (equal pointers and strides, src_pages = dst_pages) or do not
- *              overlap, and no two of the destinations overlap.
+ *              overlap, and no destination overlaps another pool. Pools may be interleaved in one
+ *              buffer, as the decode's: as parts of one record a page and layer, of a record that
+ *              holds a page in all layers, or of a layer's share of the buffer.
  * src, dst     device int32 [n], n <= 2048.
  * plain        0, or 1 where the caller knows that no destination is named twice and that none is
  *              another entry's source (gdn_pages_plan's lists, gdn_pages_take's new pages), which

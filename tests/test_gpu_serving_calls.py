@@ -70,3 +70,52 @@ def test_add_norm_without_eps(cuda_device, dt, res, T, D):
     check(name, "dres", R.worst(dres, ref["dres"], ref["dres"].abs() * R.HALF[res] + ref["dres_abs"] * k + 1e-30), 1.0)
     check(name, "dx", R.worst(dx, ref["dx"], ref["dx"].abs() * R.HALF[dt] + ref["dres_abs"] * k + 1e-30), 1.0)
     check(name, "dw", R.worst(dw, ref["dw"], ref["dw_abs"] * (T / 592 + 200) * R.U + 1e-30), 1.0)
+
+
+def shared_buffer(dev, layout, P, L, taps, vals, seed):
+    """(buffer, taps pool, states pool), [L, P, page] views that lie in one buffer of fp32."""
+    gen = torch.Generator().manual_seed(seed)
+    make = lambda *s: torch.randint(-99, 99, s, generator=gen).float().to(dev)  # noqa: E731
+    if layout == "layer, page, record":
+        buf = make(L, P, taps + vals + 4)
+        return buf, buf[..., :taps], buf[..., taps:taps + vals]
+    if layout == "page, layer, record":
+        buf = make(P, L, taps + vals)
+        return buf, buf[..., :taps].movedim(0, 1), buf[..., taps:].movedim(0, 1)
+    if layout == "page, kind, layer":
+        buf = make(P, L * (taps + vals))
+        return (buf, buf[:, :L * taps].unflatten(1, (L, taps)).movedim(0, 1),
+                buf[:, L * taps:].unflatten(1, (L, vals)).movedim(0, 1))
+    buf = make(L, P * (taps + vals))                        # layer, kind, page
+    return buf, buf[:, :P * taps].unflatten(1, (P, taps)), buf[:, P * taps:].unflatten(1, (P, vals))
+
+
+LAYOUTS = ["layer, page, record", "page, layer, record", "page, kind, layer", "layer, kind, page"]
+
+
+@pytest.mark.parametrize("L", [1, 3])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_pages_of_pools_in_one_buffer(cuda_device, layout, L):
+    """Copies, forks and compactions of taps and states that are interleaved as the decode takes them."""
+    P, dev = 9, cuda_device
+    for kind in ("copy", "fork", "compact"):
+        buf, taps, vals = shared_buffer(dev, layout, P, L, 24, 100, seed=L)
+        before = [t.clone() for t in (taps, vals)]
+        gap = buf[..., 124:].clone() if layout == LAYOUTS[0] else None
+        refs = ints([0, 2, 0, 1, 1, 0, 0, 3, 0], dev)
+        if kind == "copy":
+            src, dst = [1, 2, 3, 4, 4], [2, 3, 1, 0, 8]
+            gdn.gdn_pages_copy([taps, vals], ints(src, dev), ints(dst, dev), page_dim=1)
+        elif kind == "fork":
+            src, dst = [3, 7, 3], [0, 2, 5]
+            assert gdn.gdn_pages_fork(refs, ints(src, dev), [taps, vals], page_dim=1).tolist() == dst
+            assert refs.tolist() == [1, 2, 1, 1, 1, 1, 0, 3, 0]
+        else:
+            new, _, m, n_live, src, dst = R.planned(refs.tolist(), [])
+            table = ints([7, 4, 3, 1, 0, -1, 9], dev)
+            got_map, live = gdn.gdn_pages_compact(refs, table, [taps, vals], page_dim=1)
+            assert got_map.tolist() == m and live.tolist() == [n_live] and refs.tolist() == new
+            assert table.tolist() == [m[7], m[4], m[3], m[1], -1, -1, 9]
+        for pool, was in zip((taps, vals), before):
+            assert torch.equal(pool.cpu(), R.copied(was, was, src, dst, 1)), kind
+        assert gap is None or torch.equal(buf[..., 124:], gap)

@@ -1,10 +1,14 @@
 """Strided and expanded views at the serving entry points, on the CPU: the helpers that turn a
 tensor's strides into those of the C ABI. There 0 stands for a dense tensor, so a tensor that is
 expanded along its tokens or pages (stride 0, and the memory of one) must never get so far."""
+import ctypes
+import random
+
 import pytest
 import torch
 
 from gated_deltanet_mixer_causal_b200 import _lib
+from gated_deltanet_mixer_causal_b200.build import build
 
 
 def test_token_strides():
@@ -54,3 +58,58 @@ def test_pages_that_share_memory_are_refused():
             _lib._pool_layout(t, "pool", 1)
     layout = _lib._pool_layout(torch.zeros(5, 3, 32).movedim(1, 0), "pool", 1)      # [layers, P, page] by strides
     assert layout == (5, 3, 128, 384, 128)
+
+
+# --------------------------------------------------------------------- pools in one buffer
+#
+# A call whose arguments pass every other check, but whose copy one launch cannot number (pages of
+# 2^44 bytes, fake addresses), is refused as unsupported, before anything is launched.
+
+UNIT = 1 << 44
+BASE = 0x7f0000000000
+
+
+def copied(first, second):
+    """The status of a copy inside each of two pools (at, bytes, page, layer, layers in units), 5 pages each."""
+    build()
+    arr = (_lib._PagePool * 2)()
+    for d, (at, size, page, layer, layers) in zip(arr, (first, second)):
+        d.src = d.dst = BASE + at * UNIT
+        d.page_bytes, d.layers = size * UNIT, layers
+        d.src_page_stride = d.dst_page_stride = page * UNIT
+        d.src_layer_stride = d.dst_layer_stride = layer * UNIT
+    return _lib.lib().gdn_pages_copy(ctypes.addressof(arr), 2, 5, 5, 64, 128, 4, 1, None)
+
+
+@pytest.mark.parametrize("first,second", [
+    ((0, 1, 3, 0, 1), (1, 2, 3, 0, 1)),                    # a record a page: [taps | state]
+    ((1, 2, 4, 0, 1), (0, 1, 4, 0, 1)),                    # the state first in the list, a gap behind
+    ((0, 1, 3, 15, 2), (1, 2, 3, 15, 2)),                  # [layer][page][taps | state]
+    ((0, 1, 6, 3, 2), (1, 2, 6, 3, 2)),                    # [page][layer][taps | state]
+    ((0, 1, 6, 1, 2), (2, 2, 6, 2, 2)),                    # [page][taps of all layers | states of all layers]
+    ((0, 1, 1, 15, 2), (5, 2, 2, 15, 2)),                  # [layer][taps of all pages | states of all pages]
+    ((0, 1, 1, 5, 2), (10, 2, 2, 10, 2)),                  # one behind the other
+])
+def test_copy_takes_pools_that_share_a_buffer(first, second):
+    assert copied(first, second) == _lib.GDN_ERR_UNSUPPORTED
+    assert copied(second, first) == _lib.GDN_ERR_UNSUPPORTED
+
+
+def test_copy_takes_no_pools_that_overlap():
+    """Random layouts of two pools: what passes has no unit of memory in both."""
+    rng, passed = random.Random(7), 0
+    for _ in range(4000):
+        page, layers = rng.randint(1, 8), rng.randint(1, 3)
+        specs = []
+        for _ in range(2):
+            size = rng.randint(1, 3)
+            p = page if rng.random() < 0.6 else rng.randint(size, 8)
+            specs.append((rng.randint(0, 12), size, p, rng.choice([p * 5, page * 5, page, size, rng.randint(1, 40)]), layers))
+        held = [{at + l * layer + p * stride + i for l in range(n) for p in range(5) for i in range(size)}
+                for at, size, stride, layer, n in specs]
+        status = copied(*specs)
+        assert status in (_lib.GDN_ERR_INVALID_ARG, _lib.GDN_ERR_UNSUPPORTED)
+        if status == _lib.GDN_ERR_UNSUPPORTED:
+            assert not held[0] & held[1], specs
+            passed += 1
+    assert passed > 200
