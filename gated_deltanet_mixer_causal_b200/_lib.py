@@ -57,6 +57,8 @@ SIGNATURES = {
     "gdn_pages_take": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P]),
     "gdn_pages_ref": (ctypes.c_int, [_P, _I32, _P, _I32, _I32, _P]),
     "gdn_pages_plan": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _P, _P, _P]),
+    "gdn_pages_fork": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _I32, _P]),
+    "gdn_pages_compact": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _P, _P, _P, _I32, _P]),
     "gdn_gated_norm": (ctypes.c_int, [_P, _P, _I64, _P, _F32, _P, ctypes.c_int, _I64, _I32, _I32, _P]),
     "gdn_gated_norm_bwd": (ctypes.c_int, [_P, _P, _I64, _P, _F32, _P, _P, _P, _I64, _P, ctypes.c_int,
                                           _I64, _I32, _I32, _P, _SZ, _P]),
@@ -561,7 +563,7 @@ def _pool_list(pools):
 
 
 def _describe_counted(refs: torch.Tensor, pools, page_dim: int):
-    """_describe for pools whose pages ``refs`` counts, before anything is changed."""
+    """_describe for pools whose pages ``refs`` counts."""
     pools = _pool_list(pools)
     desc, pages, _ = _describe(pools, pools, page_dim, _device_of(refs, "refs"))
     if pages != refs.numel():
@@ -617,16 +619,21 @@ def gdn_pages_ref(refs: torch.Tensor, pages: torch.Tensor, delta: int) -> None:
 def gdn_pages_fork(refs: torch.Tensor, src: torch.Tensor, pools, page_dim: int = 0,
                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """A new page for each entry of ``src`` (see ``gdn_pages_take``), holding a copy of page
-    src[i] in each pool of ``pools``. Returns the new pages."""
+    src[i] in each pool of ``pools``. Returns the new pages. A refused call changes nothing."""
     desc, P = _describe_counted(refs, pools, page_dim)
-    out = gdn_pages_take(refs, src=src, out=out)
-    _call(refs.device, "gdn_pages_copy", ctypes.addressof(desc), len(desc), P, P, src.data_ptr(), out.data_ptr(),
-          src.numel(), 1)
+    dev, n = refs.device, src.numel()
+    _want(refs, "refs", (P,), torch.int32, dev)
+    _want(src, "src", (n,), torch.int32, dev)
+    if out is None:
+        out = torch.empty((n,), dtype=torch.int32, device=dev)
+    else:
+        _want(out, "out", (n,), torch.int32, dev)
+    _call(dev, "gdn_pages_fork", refs.data_ptr(), P, src.data_ptr(), n, out.data_ptr(), ctypes.addressof(desc), len(desc))
     return out
 
 
-def _plan(refs: torch.Tensor, table: Optional[torch.Tensor]):
-    """(src | dst | map | n_live in one tensor, P / 2)"""
+def _plan_lists(refs: torch.Tensor, table: Optional[torch.Tensor]):
+    """What gdn_pages_plan writes, src | dst | map | n_live in one tensor, and the call's arguments."""
     dev, P = _device_of(refs, "refs"), refs.numel()
     _want(refs, "refs", (P,), torch.int32, dev)
     if table is not None:
@@ -634,30 +641,25 @@ def _plan(refs: torch.Tensor, table: Optional[torch.Tensor]):
     half = P // 2
     lists = torch.empty((2 * half + P + 1,), dtype=torch.int32, device=dev)
     at = lists.data_ptr()
-    _call(dev, "gdn_pages_plan", refs.data_ptr(), P, _addr(table), 0 if table is None else table.numel(),
-          at, at + 4 * half, at + 8 * half, at + 8 * half + 4 * P)
-    return lists, half
+    return lists, half, (refs.data_ptr(), P, _addr(table), 0 if table is None else table.numel(),
+                         at, at + 4 * half, at + 8 * half, at + 8 * half + 4 * P)
 
 
 def gdn_pages_plan(refs: torch.Tensor, table: Optional[torch.Tensor] = None):
     """The moves that bring the live pages (count > 0) to the front: (src, dst, map, n_live), the
     lists padded with -1; refs and the page numbers in ``table`` (any shape) are rewritten."""
-    lists, half = _plan(refs, table)
+    lists, half, args = _plan_lists(refs, table)
+    _call(refs.device, "gdn_pages_plan", *args)
     return lists[:half], lists[half:2 * half], lists[2 * half:-1], lists[-1:]
-
-
-_MAX_LIST = 2048     # entries of one gdn_pages_copy call
 
 
 def gdn_pages_compact(refs: torch.Tensor, table: Optional[torch.Tensor], pools, page_dim: int = 0):
     """Bring the live pages to the front of every pool: ``refs`` and ``table`` are rewritten.
-    Returns (map [P]: each live page's new place, -1 for free ones; n_live [1]), on the device."""
-    desc, P = _describe_counted(refs, pools, page_dim)
-    lists, half = _plan(refs, table)
-    at = lists.data_ptr()
-    for i in range(0, half, _MAX_LIST):
-        _call(refs.device, "gdn_pages_copy", ctypes.addressof(desc), len(desc), P, P, at + 4 * i, at + 4 * (half + i),
-              min(_MAX_LIST, half - i), 1)
+    Returns (map [P]: each live page's new place, -1 for free ones; n_live [1]), on the device.
+    A refused call changes nothing."""
+    desc, _ = _describe_counted(refs, pools, page_dim)
+    lists, half, args = _plan_lists(refs, table)
+    _call(refs.device, "gdn_pages_compact", *args, ctypes.addressof(desc), len(desc))
     return lists[2 * half:-1], lists[-1:]
 
 

@@ -485,15 +485,16 @@ gdn_status_t gdn_decode_paged(const void* x, int64_t x_stride, const void* conv_
                      "decode_paged launch");
 }
 
-gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32_t src_pages,
-                            int32_t dst_pages, const int32_t* src, const int32_t* dst, int32_t n,
-                            int32_t plain, gdn_stream_t stream) {
+// The checks of a copy, before anything is launched; `a` becomes its launch, of no pool where there is
+// nothing to copy.
+static gdn_status_t pages_copy_args(gdn::PagesCopy& a, const gdn_page_pool_t* pools, int32_t n_pools, int32_t src_pages,
+                                    int32_t dst_pages, const int32_t* src, const int32_t* dst, int32_t n, bool plain) {
   if (n < 0 || src_pages < 0 || dst_pages < 0) return fail(GDN_ERR_INVALID_ARG, "pages_copy: negative count");
   if (n_pools < 1 || n_pools > gdn::kPagesMaxPools || !pools)
     return fail(GDN_ERR_INVALID_ARG, "pages_copy: %d pools, expected 1 to %d", n_pools, gdn::kPagesMaxPools);
   if (n > gdn::kPagesMaxList)
     return fail(GDN_ERR_UNSUPPORTED, "pages_copy: %d entries, at most %d a call", n, gdn::kPagesMaxList);
-  gdn::PagesCopy a{};
+  a = {};
   a.src_pages = src_pages; a.dst_pages = dst_pages; a.src = src; a.dst = dst; a.n = n;
   Pages from[gdn::kPagesMaxPools] = {}, to[gdn::kPagesMaxPools] = {};
   for (int i = 0; i < n_pools; ++i) {
@@ -526,23 +527,41 @@ gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32
     a.pool[a.n_pools++] = {(const char*)p.src, (char*)p.dst, p.page_bytes, p.src_page_stride, p.src_layer_stride,
                            p.dst_page_stride, p.dst_layer_stride, p.layers, same};
   }
+  if (a.n_pools > 0 && !gdn::pages_copy_fits(a, plain))
+    return fail(GDN_ERR_UNSUPPORTED, "pages_copy: too much for one launch; split the list");
+  return GDN_OK;
+}
+
+gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32_t src_pages,
+                            int32_t dst_pages, const int32_t* src, const int32_t* dst, int32_t n,
+                            int32_t plain, gdn_stream_t stream) {
+  gdn::PagesCopy a;
+  const gdn_status_t s = pages_copy_args(a, pools, n_pools, src_pages, dst_pages, src, dst, n, plain != 0);
+  if (s != GDN_OK) return s;
   if (a.n_pools == 0) return ok();
-  if (!gdn::pages_copy_fits(a, plain != 0)) return fail(GDN_ERR_UNSUPPORTED, "pages_copy: too much for one launch; split the list");
   return cuda_status(gdn::launch_pages_copy(a, plain != 0, (cudaStream_t)stream), "pages_copy launch");
 }
 
-gdn_status_t gdn_pages_take(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n, int32_t* out,
-                            gdn_stream_t stream) {
+static gdn_status_t pages_take_args(const int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n,
+                                    const int32_t* out) {
   if (n < 0 || n_pages < 0) return fail(GDN_ERR_INVALID_ARG, "pages_take: negative count");
   if (n > gdn::kPagesMaxList)
     return fail(GDN_ERR_UNSUPPORTED, "pages_take: %d entries, at most %d a call", n, gdn::kPagesMaxList);
-  if (n == 0) return ok();
+  if (n == 0) return GDN_OK;
   if (!out || (n_pages > 0 && !refs)) return fail(GDN_ERR_INVALID_ARG, "pages_take: refs and out must be non-null");
   if (!aligned4(refs) || !aligned4(src) || !aligned4(out))
     return fail(GDN_ERR_INVALID_ARG, "pages_take: arrays must be 4-byte aligned");
   if (overlap(out, (size_t)n * 4, refs, (size_t)n_pages * 4) || overlap(out, (size_t)n * 4, src, (size_t)n * 4) ||
       overlap(src, (size_t)n * 4, refs, (size_t)n_pages * 4))
     return fail(GDN_ERR_INVALID_ARG, "pages_take: arrays overlap");
+  return GDN_OK;
+}
+
+gdn_status_t gdn_pages_take(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n, int32_t* out,
+                            gdn_stream_t stream) {
+  const gdn_status_t s = pages_take_args(refs, n_pages, src, n, out);
+  if (s != GDN_OK) return s;
+  if (n == 0) return ok();
   return cuda_status(gdn::launch_pages_take(refs, n_pages, src, n, out, (cudaStream_t)stream), "pages_take launch");
 }
 
@@ -557,8 +576,8 @@ gdn_status_t gdn_pages_ref(int32_t* refs, int32_t n_pages, const int32_t* pages,
   return cuda_status(gdn::launch_pages_ref(refs, n_pages, pages, n, delta, (cudaStream_t)stream), "pages_ref launch");
 }
 
-gdn_status_t gdn_pages_plan(int32_t* refs, int32_t n_pages, int32_t* table, int32_t n_table, int32_t* src,
-                            int32_t* dst, int32_t* map, int32_t* n_live, gdn_stream_t stream) {
+static gdn_status_t pages_plan_args(const int32_t* refs, int32_t n_pages, const int32_t* table, int32_t n_table,
+                                    const int32_t* src, const int32_t* dst, const int32_t* map, const int32_t* n_live) {
   if (n_table < 0 || n_pages < 0) return fail(GDN_ERR_INVALID_ARG, "pages_plan: negative count");
   if (!n_live || (n_pages > 0 && (!refs || !map)) || (n_pages > 1 && (!src || !dst)) || (n_table > 0 && !table))
     return fail(GDN_ERR_INVALID_ARG, "pages_plan: refs, src, dst, map, n_live (and table) must be non-null");
@@ -570,8 +589,76 @@ gdn_status_t gdn_pages_plan(int32_t* refs, int32_t n_pages, int32_t* table, int3
     for (int j = 0; j < i; ++j)
       if (overlap(arr[i], by[i], arr[j], by[j])) return fail(GDN_ERR_INVALID_ARG, "pages_plan: arrays overlap");
   }
+  return GDN_OK;
+}
+
+gdn_status_t gdn_pages_plan(int32_t* refs, int32_t n_pages, int32_t* table, int32_t n_table, int32_t* src,
+                            int32_t* dst, int32_t* map, int32_t* n_live, gdn_stream_t stream) {
+  const gdn_status_t s = pages_plan_args(refs, n_pages, table, n_table, src, dst, map, n_live);
+  if (s != GDN_OK) return s;
   return cuda_status(gdn::launch_pages_plan(refs, n_pages, table, n_table, src, dst, map, n_live, (cudaStream_t)stream),
                      "pages_plan launch");
+}
+
+// What a call that changes counts before it copies asks of the pools besides: each is copied within
+// itself, and [p, p + bytes) of its counts and lists lies outside.
+static bool copies_within(const gdn::PagesCopy& a) {
+  for (int i = 0; i < a.n_pools; ++i)
+    if (!a.pool[i].same) return false;
+  return true;
+}
+static bool in_pools(const gdn::PagesCopy& a, const void* p, size_t bytes) {
+  for (int i = 0; i < a.n_pools; ++i) {
+    const gdn::PagePool& q = a.pool[i];
+    if (overlap(p, bytes, q.dst, Pages{q.dst, q.page_bytes, q.dst_page, q.dst_layer, a.dst_pages, q.layers}.extent()))
+      return true;
+  }
+  return false;
+}
+
+gdn_status_t gdn_pages_fork(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n, int32_t* out,
+                            const gdn_page_pool_t* pools, int32_t n_pools, gdn_stream_t stream) {
+  gdn_status_t s = pages_take_args(refs, n_pages, src, n, out);
+  if (s != GDN_OK) return s;
+  if (n > 0 && !src) return fail(GDN_ERR_INVALID_ARG, "pages_fork: src must be non-null");
+  gdn::PagesCopy a;
+  s = pages_copy_args(a, pools, n_pools, n_pages, n_pages, src, out, n, true);
+  if (s != GDN_OK) return s;
+  if (!copies_within(a)) return fail(GDN_ERR_INVALID_ARG, "pages_fork: a pool's src and dst differ");
+  if (in_pools(a, refs, (size_t)n_pages * 4)) return fail(GDN_ERR_INVALID_ARG, "pages_fork: refs overlaps a pool");
+  if (n == 0) return ok();
+  s = cuda_status(gdn::launch_pages_take(refs, n_pages, src, n, out, (cudaStream_t)stream), "pages_fork: taking pages");
+  if (s != GDN_OK || a.n_pools == 0) return s;
+  return cuda_status(gdn::launch_pages_copy(a, true, (cudaStream_t)stream), "pages_fork: copying pages");
+}
+
+gdn_status_t gdn_pages_compact(int32_t* refs, int32_t n_pages, int32_t* table, int32_t n_table, int32_t* src,
+                               int32_t* dst, int32_t* map, int32_t* n_live, const gdn_page_pool_t* pools,
+                               int32_t n_pools, gdn_stream_t stream) {
+  gdn_status_t s = pages_plan_args(refs, n_pages, table, n_table, src, dst, map, n_live);
+  if (s != GDN_OK) return s;
+  const int32_t half = n_pages / 2, most = gdn::kPagesMaxList;
+  gdn::PagesCopy a;
+  s = pages_copy_args(a, pools, n_pools, n_pages, n_pages, src, dst, half < most ? half : most, true);
+  if (s != GDN_OK) return s;
+  if (!copies_within(a)) return fail(GDN_ERR_INVALID_ARG, "pages_compact: a pool's src and dst differ");
+  if (half > most && half % most != 0 && a.n_pools > 0) {       // the last part, which may be cut into more tiles
+    gdn::PagesCopy b = a;
+    b.n = half % most;
+    if (!gdn::pages_copy_fits(b, true)) return fail(GDN_ERR_UNSUPPORTED, "pages_compact: too much for one launch");
+  }
+  if (in_pools(a, refs, (size_t)n_pages * 4) || in_pools(a, table, (size_t)n_table * 4) ||
+      in_pools(a, src, (size_t)half * 4) || in_pools(a, dst, (size_t)half * 4) ||
+      in_pools(a, map, (size_t)n_pages * 4) || in_pools(a, n_live, 4))
+    return fail(GDN_ERR_INVALID_ARG, "pages_compact: counts, lists or table overlap a pool");
+  s = cuda_status(gdn::launch_pages_plan(refs, n_pages, table, n_table, src, dst, map, n_live, (cudaStream_t)stream),
+                  "pages_compact: planning");
+  // the plan's sources and destinations are distinct, so a long list is copied in parts
+  for (int32_t i = 0; s == GDN_OK && a.n_pools > 0 && i < half; i += most) {
+    a.src = src + i; a.dst = dst + i; a.n = half - i < most ? half - i : most;
+    s = cuda_status(gdn::launch_pages_copy(a, true, (cudaStream_t)stream), "pages_compact: copying pages");
+  }
+  return s;
 }
 
 size_t gdn_norm_bwd_workspace_size(int32_t D) { return D > 0 ? (size_t)D * gdn::kNormParts * sizeof(float) : 0; }

@@ -426,8 +426,8 @@ gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32
  *
  * gdn_pages_take: out[i] (device int32 [n], n <= 2048) receives the lowest free page not taken
  *   before it, whose count becomes 1, for i = 0, 1, ...; -1 once none is free. With src (device
- *   int32 [n]) an entry whose src[i] is not a page that is in use gets -1 and takes none:
- *   gdn_pages_copy(src, out, plain) then completes a fork.
+ *   int32 [n]) an entry whose src[i] is not a page that is in use gets -1 and takes none
+ *   (gdn_pages_fork copies the pages too).
  * gdn_pages_ref: refs[pages[i]] += delta for every entry that is a page (a page listed twice
  *   counts twice); counts below 0 become 0. delta = 1 shares pages, -1 frees them.
  * gdn_pages_plan: the moves that bring the live pages to the front: with n_live of them, the
@@ -447,6 +447,20 @@ gdn_status_t gdn_pages_ref(int32_t* refs, int32_t n_pages, const int32_t* pages,
 gdn_status_t gdn_pages_plan(int32_t* refs, int32_t n_pages, int32_t* table, int32_t n_table,
                             int32_t* src, int32_t* dst, int32_t* map, int32_t* n_live,
                             gdn_stream_t stream);
+
+/*
+ * gdn_pages_fork, gdn_pages_compact -- the counts and the pages in one call: gdn_pages_take with
+ * src and the copy of page src[i] to the page taken; gdn_pages_plan and the copy of its moves.
+ * pools: n_pools descriptions (gdn_pages_copy) of n_pages pages each, src and dst the same pool.
+ * Everything is checked before anything is launched, so a refused call leaves counts, tables and
+ * pages as they were. refs and the lists lie outside the pools. Two launches (for compaction one
+ * more for every further 2048 moves). Return codes of the calls that they are made of.
+ */
+gdn_status_t gdn_pages_fork(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n, int32_t* out,
+                            const gdn_page_pool_t* pools, int32_t n_pools, gdn_stream_t stream);
+gdn_status_t gdn_pages_compact(int32_t* refs, int32_t n_pages, int32_t* table, int32_t n_table,
+                               int32_t* src, int32_t* dst, int32_t* map, int32_t* n_live,
+                               const gdn_page_pool_t* pools, int32_t n_pools, gdn_stream_t stream);
 
 /*
  * gdn_gated_norm -- the norm and gate of the mixer's output, per token and value head:

@@ -119,3 +119,20 @@ def test_pages_of_pools_in_one_buffer(cuda_device, layout, L):
         for pool, was in zip((taps, vals), before):
             assert torch.equal(pool.cpu(), R.copied(was, was, src, dst, 1)), kind
         assert gap is None or torch.equal(buf[..., 124:], gap)
+
+
+@pytest.mark.parametrize("kind", ["fork", "compact"])
+def test_refused_forks_and_compactions_change_nothing(cuda_device, kind):
+    """What only the copy's own checks find: the same pool twice, pools that overlap, layers that do."""
+    dev = cuda_device
+    buf = torch.arange(8 * 64, dtype=FP, device=dev)
+    pool, kept = buf[:256].view(8, 32), buf.clone()
+    refs, table = ints([0, 1, 0, 2, 1, 0, 0, 1], dev), ints([7, 4, 3, 1], dev)
+    for bad, dim in (([pool, pool], 0), ([pool, buf[128:384].view(8, 32)], 0),
+                     (buf.as_strided((2, 8, 32), (32, 32, 1)), 1), ([pool[:, :16], pool[:, 12:28]], 0)):
+        with pytest.raises(gdn.GDNError):
+            if kind == "fork":
+                gdn.gdn_pages_fork(refs, ints([3, 1], dev), bad, page_dim=dim)
+            else:
+                gdn.gdn_pages_compact(refs, table, bad, page_dim=dim)
+        assert refs.tolist() == [0, 1, 0, 2, 1, 0, 0, 1] and table.tolist() == [7, 4, 3, 1] and torch.equal(buf, kept)

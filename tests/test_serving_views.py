@@ -113,3 +113,51 @@ def test_copy_takes_no_pools_that_overlap():
             assert not held[0] & held[1], specs
             passed += 1
     assert passed > 200
+
+
+# ------------------------------------------------- forks and compactions that are refused
+#
+# The counts are changed before the pages are copied, so a call that the copy would refuse must end
+# before its first launch. Without a GPU a launch fails with a CUDA error, so a refusal shows that
+# none was tried; with one, the arguments below are all refused and none is launched either.
+
+def refused(kind, *specs, P=8, n=3, refs=1 << 20, src=2 << 20, out=3 << 20, table=4 << 20):
+    build()
+    L = _lib.lib()
+    arr = (_lib._PagePool * max(len(specs), 1))()
+    for d, s in zip(arr, specs):
+        v = dict(src=BASE, dst=BASE, page_bytes=4096, src_page_stride=0, src_layer_stride=0, dst_page_stride=0,
+                 dst_layer_stride=0, layers=1)
+        v.update(s)
+        for k, x in v.items():
+            setattr(d, k, x)
+    at = ctypes.addressof(arr)
+    if kind == "fork":
+        return L.gdn_pages_fork(refs, P, src, n, out, at, len(specs), None)
+    return L.gdn_pages_compact(refs, P, table, 4, src, out, 5 << 20, 6 << 20, at, len(specs), None)
+
+
+@pytest.mark.parametrize("kind", ["fork", "compact"])
+def test_refused_before_the_counts_change(kind):
+    INVALID, UNSUPPORTED = _lib.GDN_ERR_INVALID_ARG, _lib.GDN_ERR_UNSUPPORTED
+    far = BASE + (1 << 40)
+    assert refused(kind, {}, {}) == INVALID                                   # one pool twice
+    assert refused(kind, {}, dict(src=BASE + 4096, dst=BASE + 4096)) == INVALID
+    assert refused(kind, dict(src=BASE + 8, dst=BASE + 8)) == INVALID and refused(kind, dict(page_bytes=40)) == INVALID
+    assert refused(kind, dict(src=far)) == INVALID                            # from another pool
+    assert refused(kind, dict(src=None, dst=None)) == INVALID and refused(kind) == INVALID
+    assert refused(kind, dict(src_page_stride=64, dst_page_stride=64)) == INVALID
+    assert refused(kind, dict(layers=2, src_layer_stride=16, dst_layer_stride=16)) == INVALID
+    assert refused(kind, dict(page_bytes=UNIT)) == UNSUPPORTED                # too much for one launch
+    assert refused(kind, {}, refs=BASE + 64) == INVALID and refused(kind, {}, src=BASE + 64) == INVALID
+    assert refused(kind, {}, out=BASE + 64) == INVALID and refused(kind, {}, out=(1 << 20) + 4) == INVALID
+    assert refused(kind, {}, refs=None) == INVALID and refused(kind, {}, src=None) == INVALID
+    assert refused(kind, {}, out=None) == INVALID and refused(kind, {}, P=-1) == INVALID
+    if kind == "fork":
+        assert refused(kind, {}, n=2049) == UNSUPPORTED and refused(kind, {}, n=-1) == INVALID
+        assert refused(kind, {}, n=0) == _lib.GDN_OK
+    else:
+        assert refused(kind, {}, table=BASE + 64) == INVALID and refused(kind, {}, table=(1 << 20) + 4) == INVALID
+        # 4,096 entries in two parts of 64 groups each, 16 tiles a layer, and 992 more, 31 tiles a layer
+        deep = dict(page_bytes=512, src_layer_stride=512 * 20000, dst_layer_stride=512 * 20000, layers=100_000_000)
+        assert refused(kind, deep, P=2 * (4096 + 992), refs=1 << 58, src=1 << 59, out=3 << 58, table=5 << 58) == UNSUPPORTED
