@@ -307,7 +307,8 @@ int64_t plain_ctas(const PagesCopy& a, CopyTiles& t) {
   for (int k = 0; k < a.n_pools; ++k) {
     const PlainShape s = plain_shape(a.pool[k].page_bytes, a.n);
     t.first[k] = (uint32_t)ctas;
-    ctas += (int64_t)s.cols * s.step * a.pool[k].layers;
+    const int64_t cols = (a.pool[k].page_bytes + (1LL << s.lw) - 1) >> s.lw;     // s.cols may have wrapped
+    ctas += cols * s.step * a.pool[k].layers;
   }
   return ctas;
 }

@@ -149,6 +149,7 @@ def test_refused_before_the_counts_change(kind):
     assert refused(kind, dict(src_page_stride=64, dst_page_stride=64)) == INVALID
     assert refused(kind, dict(layers=2, src_layer_stride=16, dst_layer_stride=16)) == INVALID
     assert refused(kind, dict(page_bytes=UNIT)) == UNSUPPORTED                # too much for one launch
+    assert refused(kind, dict(page_bytes=4 * UNIT)) == UNSUPPORTED            # 2^32 tiles
     assert refused(kind, {}, refs=BASE + 64) == INVALID and refused(kind, {}, src=BASE + 64) == INVALID
     assert refused(kind, {}, out=BASE + 64) == INVALID and refused(kind, {}, out=(1 << 20) + 4) == INVALID
     assert refused(kind, {}, refs=None) == INVALID and refused(kind, {}, src=None) == INVALID
