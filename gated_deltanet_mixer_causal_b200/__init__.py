@@ -26,7 +26,7 @@ from ._lib import (GDNError, LIB_PATH, gdn_chunk_prefill, gdn_chunk_prefill_noal
                    gdn_decode_tokens, gdn_prefill_noalloc_status, gdn_prefill_status, lib,
                    gdn_decode_paged, gdn_pages_copy, gdn_pages_take, gdn_pages_ref, gdn_pages_fork,
                    gdn_pages_plan, gdn_pages_compact, gdn_gated_norm, gdn_gated_norm_bwd, gdn_add_norm,
-                   gdn_add_norm_bwd, gdn_norm_bwd_workspace_size)
+                   gdn_add_norm_bwd, gdn_norm_bwd_workspace_size, _check_gate)
 
 __all__ = ["GDNError", "LIB_PATH", "lib", "gdn_conv1d_silu", "gdn_chunk_prefill",
            "gdn_chunk_prefill_workspace_size", "gdn_chunk_prefill_noalloc", "gdn_chunk_prefill_path", "gdn_chunk_prefill_launches", "gdn_decode_step",
@@ -61,6 +61,10 @@ def prefill_layer(x: torch.Tensor, conv_w: torch.Tensor, g: torch.Tensor, beta: 
     (``gdn_gated_norm``), as ``gdn_decode_paged`` does for single tokens."""
     if (z is None) != (norm_w is None):
         raise ValueError("z and norm_w come together")
+    if z is not None:                # before the states and taps advance
+        if o is None:
+            o = torch.empty((x.shape[0], Hv, d), dtype=x.dtype, device=x.device)
+        _check_gate(o, z, norm_w, eps)
     y = gdn_conv1d_silu(x, conv_w, cu_seqlens, conv_state_in, conv_state_out, y)
     q, k, v = qkv_views(y, Hk, Hv, d)
     o = gdn_chunk_prefill(q, k, v, g, beta, cu_seqlens, initial_state, final_state, scale,

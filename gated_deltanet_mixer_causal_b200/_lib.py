@@ -677,6 +677,22 @@ def _norm_workspace(D: int, workspace: Optional[torch.Tensor], device):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _check_gate(o: torch.Tensor, z: torch.Tensor, w: torch.Tensor, eps: float) -> None:
+    """Raises what gdn_gated_norm(o, z, w, eps, y=o) would raise, and launches nothing."""
+    dev, dt, shape = _device_of(o, "o"), o.dtype, o.shape
+    T, Hv, dv = shape
+    _want(o, "o", shape, dt, dev)
+    _want_view(z, "z", shape, dt, dev)
+    _want(w, "w", (dv,), dt, dev)
+    stride = _token_rows(z, "z", 1)
+    _call(dev, "gdn_gated_norm", o.data_ptr(), z.data_ptr(), stride, w.data_ptr(), eps, o.data_ptr(), _dtype_code(o), 0,
+          Hv, dv)                                                # a call of no tokens checks all but overlaps
+    es, row, at = o.element_size(), Hv * dv, o.data_ptr()
+    for name, t, size in (("z", z, (T - 1) * (stride or row) + row), ("w", w, dv)):
+        if T > 0 and at < t.data_ptr() + size * es and t.data_ptr() < at + T * row * es:
+            raise GDNError(GDN_ERR_INVALID_ARG, "gdn_gated_norm", f"o overlaps {name}")
+
+
 def gdn_gated_norm(o: torch.Tensor, z: torch.Tensor, w: torch.Tensor, eps: float = 1e-6,
                    y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """o / sqrt(mean(o^2) + eps) * w * SiLU(z) over the last dimension: o [T, Hv, dv], z the same

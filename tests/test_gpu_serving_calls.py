@@ -136,3 +136,27 @@ def test_refused_forks_and_compactions_change_nothing(cuda_device, kind):
             else:
                 gdn.gdn_pages_compact(refs, table, bad, page_dim=dim)
         assert refs.tolist() == [0, 1, 0, 2, 1, 0, 0, 1] and table.tolist() == [7, 4, 3, 1] and torch.equal(buf, kept)
+
+
+@pytest.mark.parametrize("act", [BF, FP])
+def test_prefill_layer_refuses_a_gate_before_it_computes(cuda_device, act):
+    dev, Hk, Hv, d, T = cuda_device, 2, 4, 32, 24
+    c = case(dev, 1, T, Hk, Hv, d, act, FP, 2, seed=5, gate=True)
+    x, z, g, beta = (c[k].squeeze(0) for k in ("x", "z", "g", "beta"))
+    w, zeros = c["norm_w"], torch.zeros(T * Hv * d + 8, dtype=act, device=dev)
+    state, conv = torch.full((1, Hv, d, d), 3.0, device=dev), torch.full((1, 3, 8 * d), 3.0, dtype=act, device=dev)
+    bad = [dict(z=z[1:]), dict(z=z.half()), dict(z=z.cpu()), dict(z=z.transpose(1, 2).contiguous().transpose(1, 2)),
+           dict(z=z[:1].expand(T, Hv, d)), dict(norm_w=w[:16]), dict(norm_w=w.double()), dict(eps=-1.0), dict(norm_w=None),
+           dict(z=zeros[1:T * Hv * d + 1].view(T, Hv, d)), dict(o=z), dict(z=None),
+           dict(z=torch.zeros(T, Hv * d + 4, dtype=act, device=dev)[:, :Hv * d].unflatten(1, (Hv, d)))]
+    run = lambda **kw: gdn.prefill_layer(x, c["conv_w"], g, beta, Hk, Hv, d, final_state=state, conv_state_out=conv,  # noqa: E731
+                                         **{**dict(z=z, norm_w=w), **kw})
+    for kw in bad:
+        with pytest.raises((ValueError, gdn.GDNError)):
+            run(**kw)
+    torch.cuda.synchronize()
+    assert (state == 3.0).all() and (conv == 3.0).all()
+    o = run()
+    assert torch.equal(run(o=torch.empty_like(o)), o) and not (state == 3.0).any()
+    empty = gdn.prefill_layer(x[:0], c["conv_w"], g[:0], beta[:0], Hk, Hv, d, z=z[:0], norm_w=w)
+    assert empty.shape == (0, Hv, d)
