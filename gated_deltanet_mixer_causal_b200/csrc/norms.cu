@@ -25,6 +25,9 @@
 namespace gdn {
 namespace {
 
+// No input is `const __restrict__`: these kernels begin while the grid before them, which may have
+// made their inputs, still runs, and the qualifier would let their loads move ahead of the wait.
+
 constexpr int kGatedThreads = 256;
 constexpr int kGatedWarps = kGatedThreads / 32;
 constexpr int kGatedBwdBlocks = 3;    // resident CTAs per SM of the backward pass
@@ -114,7 +117,7 @@ __device__ __forceinline__ uint2 div_rows(uint32_t r, uint32_t H, uint32_t magic
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kGatedThreads, 4)
-gated_norm_kernel(const T* o, const T* __restrict__ z, int64_t z_stride, const T* __restrict__ w, float eps, T* y,
+gated_norm_kernel(const T* o, const T* z, int64_t z_stride, const T* w, float eps, T* y,
                   uint32_t rows, uint32_t H, uint32_t magic) {
   constexpr int VEC = 16 / sizeof(T), LANES = D / VEC, RPW = 32 / LANES, U = 4;
   allow_next_grid();
@@ -152,7 +155,7 @@ gated_norm_kernel(const T* o, const T* __restrict__ z, int64_t z_stride, const T
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kGatedThreads, kGatedBwdBlocks)
-gated_norm_bwd_kernel(const T* __restrict__ o, const T* __restrict__ z, int64_t z_stride, const T* __restrict__ w,
+gated_norm_bwd_kernel(const T* o, const T* z, int64_t z_stride, const T* w,
                       float eps, const T* dy, T* dout, T* __restrict__ dz, int64_t dz_stride,
                       float* __restrict__ part, uint32_t rows, uint32_t H, uint32_t magic) {
   constexpr int VEC = 16 / sizeof(T), LANES = D / VEC, RPW = 32 / LANES, U = 2;
@@ -228,7 +231,7 @@ gated_norm_bwd_kernel(const T* __restrict__ o, const T* __restrict__ z, int64_t 
 
 // dw[c] = sum over the CTAs' parts, in a fixed order: 32 columns x 32 slices of the parts a CTA
 __global__ void __launch_bounds__(1024)
-norm_dw_kernel(const float* __restrict__ part, int n_part, int D, float* __restrict__ dw) {
+norm_dw_kernel(const float* part, int n_part, int D, float* __restrict__ dw) {
   __shared__ float acc[32][33];
   allow_next_grid();
   wait_for_previous_grid();
@@ -324,7 +327,7 @@ __device__ __forceinline__ float2 row_sum(float v, float u, float (*sm)[64], int
 
 template <typename T, typename R, int NV, int MAXT, bool ODD>
 __global__ void __launch_bounds__(MAXT)
-add_norm_kernel(const T* __restrict__ x, const R* res, const T* __restrict__ w, float scale, float w_add, float eps,
+add_norm_kernel(const T* x, const R* res, const T* w, float scale, float w_add, float eps,
                 R* h, T* __restrict__ n, int64_t rows, int D) {
   __shared__ float sm[2][64];
   allow_next_grid();
@@ -387,7 +390,7 @@ add_norm_kernel(const T* __restrict__ x, const R* res, const T* __restrict__ w, 
 // registers over them and has the next row's loads in flight while it works on one.
 template <typename T, typename R, int NV, int MAXT, int MINB, bool ODD>
 __global__ void __launch_bounds__(MAXT, MINB)
-add_norm_bwd_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* __restrict__ dn, const R* dh,
+add_norm_bwd_kernel(const R* h, const T* w, const T* dn, const R* dh,
                     float scale, float w_add, float eps, R* dres, T* __restrict__ dx,
                     float* __restrict__ part, int64_t rows, int D) {
   // the next row's dh is asked for with its h and dn where the registers allow (bf16), else once
@@ -506,7 +509,7 @@ add_norm_bwd_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* _
 // keeps the weight gradient in shared memory.
 template <typename T, typename R, bool ODD>
 __global__ void __launch_bounds__(1024, 1)
-add_norm_bwd_long_kernel(const R* __restrict__ h, const T* __restrict__ w, const T* __restrict__ dn, const R* dh,
+add_norm_bwd_long_kernel(const R* h, const T* w, const T* dn, const R* dh,
                          float scale, float w_add, float eps, R* dres, T* __restrict__ dx,
                          float* __restrict__ part, int64_t rows, int D) {
   __shared__ float sm[2][64];

@@ -160,3 +160,39 @@ def test_prefill_layer_refuses_a_gate_before_it_computes(cuda_device, act):
     assert torch.equal(run(o=torch.empty_like(o)), o) and not (state == 3.0).any()
     empty = gdn.prefill_layer(x[:0], c["conv_w"], g[:0], beta[:0], Hk, Hv, d, z=z[:0], norm_w=w)
     assert empty.shape == (0, Hv, d)
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_norms_fed_by_the_launch_before(cuda_device, dt):
+    """Each call's inputs are the outputs of the launch just before it in the stream, whose end it
+    overlaps: 30 rounds of forward and backward passes, against the same rounds with a wait behind
+    every call."""
+    T, H, d, rounds = 600, 4, 128, 30
+    gen = torch.Generator().manual_seed(11)
+    o, z, x = (torch.randn(T, H * d, generator=gen).to(dt).to(cuda_device) for _ in range(3))
+    w, wide = (torch.rand(n, generator=gen).to(dt).to(cuda_device) for n in (d, H * d))
+
+    def chain(wait):
+        a, res, kept = o.clone(), x.clone(), []
+        for _ in range(rounds):
+            y = gdn.gdn_gated_norm(a.view(T, H, d), z.view(T, H, d), w).view(T, H * d)
+            wait()
+            n, h = gdn.gdn_add_norm(y, res, wide, scale=0.5)
+            wait()
+            dx, dres, dwide = gdn.gdn_add_norm_bwd(h, wide, n, n, scale=0.5)
+            wait()
+            do, dz, dw = gdn.gdn_gated_norm_bwd(dx.view(T, H, d), dres.view(T, H, d), w, dx.view(T, H, d))
+            wait()
+            # the weight gradients of this round are weights of the next call
+            y2 = gdn.gdn_gated_norm(do, dz, dw.to(dt))
+            wait()
+            n2, _ = gdn.gdn_add_norm(y2.view(T, H * d), h, dwide.to(dt))
+            wait()
+            a, res = n2, h
+            kept += [dw, dwide, n2]
+        return kept
+
+    once = chain(lambda: None)
+    slow = chain(torch.cuda.synchronize)
+    assert all(torch.equal(p, q) for p, q in zip(once, slow))
+    assert all(torch.isfinite(t).all() for t in once)
