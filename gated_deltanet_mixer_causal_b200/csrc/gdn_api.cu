@@ -453,11 +453,11 @@ gdn_status_t gdn_decode_paged(const void* x, int64_t x_stride, const void* conv_
   if (!x || !conv_w || !read_pages || !g || !beta || !o || (n_pages > 0 && (!conv_pool || !state_pool)))
     return fail(GDN_ERR_INVALID_ARG, "decode_paged: x, conv_w, the pools, read_pages, g, beta and o must be non-null");
   if (!z != !norm_w) return fail(GDN_ERR_INVALID_ARG, "decode_paged: z and norm_w come together");
-  if (!aligned16(x) || !aligned16(conv_w) || !aligned16(conv_pool) || !aligned16(state_pool) || !aligned16(g) ||
-      !aligned16(beta) || !aligned16(z) || !aligned16(norm_w) || !aligned16(o))
+  if (!aligned16(x) || !aligned16(conv_w) || !aligned16(conv_pool) || !aligned16(state_pool) || !aligned16(z) ||
+      !aligned16(norm_w) || !aligned16(o))
     return fail(GDN_ERR_INVALID_ARG, "decode_paged: pointers must be 16-byte aligned");
-  if (!aligned4(read_pages) || !aligned4(write_pages) || !aligned4(n_valid))
-    return fail(GDN_ERR_INVALID_ARG, "decode_paged: page lists must be 4-byte aligned");
+  if (!aligned4(g) || !aligned4(beta) || !aligned4(read_pages) || !aligned4(write_pages) || !aligned4(n_valid))
+    return fail(GDN_ERR_INVALID_ARG, "decode_paged: g, beta and the page lists must be 4-byte aligned");
   const size_t es = elt_size(dt), sts = elt_size(state_dt);
   const size_t toks = (size_t)B * n_tok, pages = (size_t)n_pages;
   const size_t cb = pages ? ((pages - 1) * conv_stride + taps) * es : 0;

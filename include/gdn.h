@@ -365,7 +365,8 @@ gdn_status_t gdn_decode_tokens_ex(const void* x, const void* conv_w, void* conv_
  * n_valid      device int32 [B], clamped to [0, n_tok], or NULL (every token). What lies in the
  *              tokens behind it is not used, and nothing is written or stored for them: their
  *              rows of o stay as they were, and all of those of a sequence of none.
- * g, beta      [B, n_tok, Hv] fp32.
+ * g, beta      [B, n_tok, Hv] fp32; like the page lists and counts they need only be aligned to 4
+ *              bytes.
  * z, norm_w    both NULL, or the gate [B, n_tok, Hv, dv] (a token every z_stride elements, 0:
  *              dense) and the weight [dv], dtype dt: o is then gdn_gated_norm's result with eps.
  * o            [B, n_tok, Hv, dv] dtype dt.

@@ -8,7 +8,7 @@ import gated_deltanet_mixer_causal_b200 as gdn
 import serving_ref as R
 from parity import check
 from test_gpu_norms import add_case, add_terms, gated_case, gated_terms, slack
-from test_gpu_paged import case, ints
+from test_gpu_paged import case, ints, run_and_check
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float32
@@ -160,6 +160,15 @@ def test_prefill_layer_refuses_a_gate_before_it_computes(cuda_device, act):
     assert torch.equal(run(o=torch.empty_like(o)), o) and not (state == 3.0).any()
     empty = gdn.prefill_layer(x[:0], c["conv_w"], g[:0], beta[:0], Hk, Hv, d, z=z[:0], norm_w=w)
     assert empty.shape == (0, Hv, d)
+
+
+def test_paged_decode_of_slices(cuda_device):
+    """Sequences behind the first of a batch: with 10 value heads their g and beta begin on 8 bytes."""
+    c = case(cuda_device, 4, 1, 2, 10, 16, FP, FP, 6, seed=12)
+    for key in ("x", "g", "beta"):
+        c[key] = c[key][1:]
+    assert c["g"].data_ptr() % 16 == 8
+    run_and_check("paged slices", c, [4, 0, 2], None, None, cuda_device)
 
 
 @pytest.mark.parametrize("dt", [BF, FP])

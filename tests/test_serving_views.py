@@ -162,3 +162,21 @@ def test_refused_before_the_counts_change(kind):
         # 4,096 entries in two parts of 64 groups each, 16 tiles a layer, and 992 more, 31 tiles a layer
         deep = dict(page_bytes=512, src_layer_stride=512 * 20000, dst_layer_stride=512 * 20000, layers=100_000_000)
         assert refused(kind, deep, P=2 * (4096 + 992), refs=1 << 58, src=1 << 59, out=3 << 58, table=5 << 58) == UNSUPPORTED
+
+
+def test_gates_and_lists_need_only_their_own_alignment():
+    """A slice of 10 heads' g begins on 8 bytes. The call goes on to the refusal behind the
+    alignment (o lies in the conv's pool), so nothing is launched."""
+    build()
+    L = _lib.lib()
+    at = lambda i, off=0: BASE + (i << 36) + off  # noqa: E731
+
+    def call(g, beta, read):
+        status = L.gdn_decode_paged(at(0), 0, at(1), at(2), 0, at(3), 0, 0, 16, read, None, None, g, beta, None, 0, None,
+                                    1e-6, at(2), 1, 4, 2, 2, 10, 32, 32, 1.0, None)
+        assert status == _lib.GDN_ERR_INVALID_ARG
+        return L.gdn_last_error().decode()
+
+    assert "overlaps" in call(at(5, 40), at(6, 40), at(4, 4))
+    assert "aligned" in call(at(5, 42), at(6), at(4)) and "aligned" in call(at(5), at(6, 1), at(4))
+    assert "aligned" in call(at(5), at(6), at(4, 2))
