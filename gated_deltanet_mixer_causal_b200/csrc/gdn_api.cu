@@ -568,6 +568,8 @@ gdn_status_t gdn_pages_take(int32_t* refs, int32_t n_pages, const int32_t* src, 
 gdn_status_t gdn_pages_ref(int32_t* refs, int32_t n_pages, const int32_t* pages, int32_t n, int32_t delta,
                            gdn_stream_t stream) {
   if (n < 0 || n_pages < 0) return fail(GDN_ERR_INVALID_ARG, "pages_ref: negative count");
+  if ((int64_t)n * (delta < 0 ? -(int64_t)delta : delta) > 0x7fffffffLL)
+    return fail(GDN_ERR_UNSUPPORTED, "pages_ref: %d entries of %d may pass the range of a count", n, delta);
   if (n == 0 || n_pages == 0) return ok();
   if (!refs || !pages) return fail(GDN_ERR_INVALID_ARG, "pages_ref: refs and pages must be non-null");
   if (!aligned4(refs) || !aligned4(pages)) return fail(GDN_ERR_INVALID_ARG, "pages_ref: arrays must be 4-byte aligned");

@@ -430,7 +430,8 @@ gdn_status_t gdn_pages_copy(const gdn_page_pool_t* pools, int32_t n_pools, int32
  *   int32 [n]) an entry whose src[i] is not a page that is in use gets -1 and takes none
  *   (gdn_pages_fork copies the pages too).
  * gdn_pages_ref: refs[pages[i]] += delta for every entry that is a page (a page listed twice
- *   counts twice); counts below 0 become 0. delta = 1 shares pages, -1 frees them.
+ *   counts twice); counts below 0 become 0. delta = 1 shares pages, -1 frees them. n * |delta|
+ *   is below 2^31 (else GDN_ERR_UNSUPPORTED), and so are the counts that result.
  * gdn_pages_plan: the moves that bring the live pages to the front: with n_live of them, the
  *   i-th free page below n_live takes the i-th live page at or behind it. src, dst (device int32
  *   [n_pages / 2]) receive the moves, padded with -1, for gdn_pages_copy; refs moves with the

@@ -180,3 +180,11 @@ def test_gates_and_lists_need_only_their_own_alignment():
     assert "overlaps" in call(at(5, 40), at(6, 40), at(4, 4))
     assert "aligned" in call(at(5, 42), at(6), at(4)) and "aligned" in call(at(5), at(6, 1), at(4))
     assert "aligned" in call(at(5), at(6), at(4, 2))
+
+
+def test_counts_keep_within_their_range():
+    """Entries times delta below 2^31: the sum of a page listed by all of them does not wrap."""
+    build()
+    ref = lambda n, delta: _lib.lib().gdn_pages_ref(None, 8, 64, n, delta, None)  # noqa: E731
+    assert ref(2, -2 ** 31) == ref(2 ** 30, 2) == ref(3, 2 ** 30) == ref(1, -2 ** 31) == _lib.GDN_ERR_UNSUPPORTED
+    assert ref(1, 2 ** 31 - 1) == ref(2 ** 31 - 1, -1) == _lib.GDN_ERR_INVALID_ARG     # on to the null counts
