@@ -415,6 +415,13 @@ def _call(device: torch.device, name: str, *args):
         _check(status, name)
 
 
+def _int32(n: int, name: str) -> int:
+    """n where the C ABI takes 32 bits; ctypes would drop those above without a word."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} = {n} does not fit 32 bits")
+    return n
+
+
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -519,7 +526,7 @@ def _pool_layout(t: torch.Tensor, name: str, page_dim: int):
     if len(shape) < page_dim + 2:
         raise ValueError(f"{name} has {len(shape)} dimensions, too few for page_dim = {page_dim}")
     es, strides = t.element_size(), t.stride()
-    pages, layers = shape[page_dim], shape[0] if page_dim else 1
+    pages, layers = _int32(shape[page_dim], "pages"), _int32(shape[0], "layers") if page_dim else 1
     if pages > 1 and t.is_contiguous():
         page = strides[page_dim] * es
     else:
@@ -580,7 +587,7 @@ def gdn_pages_copy(src_pool, src: torch.Tensor, dst: torch.Tensor, dst_pool=None
     pools with equal P is copied by one call. ``plain``: no destination is named twice or is
     another entry's source (faster)."""
     froms = _pool_list(src_pool)
-    n, dev = src.numel(), _device_of(src, "src")
+    n, dev = _int32(src.numel(), "n"), _device_of(src, "src")
     _want(src, "src", (n,), torch.int32, dev)
     _want(dst, "dst", (n,), torch.int32, dev)
     desc, sp, dp = _describe(froms, froms if dst_pool is None else _pool_list(dst_pool), page_dim, dev)
@@ -594,10 +601,10 @@ def gdn_pages_take(refs: torch.Tensor, n: Optional[int] = None, src: Optional[to
     them, or one for each entry of ``src`` that is a page in use. Returns them (int32, -1: none)."""
     if (n is None) == (src is None):
         raise ValueError("give either n or src")
-    dev, P = _device_of(refs, "refs"), refs.numel()
+    n = _int32(n if src is None else src.numel(), "n")
+    dev, P = _device_of(refs, "refs"), _int32(refs.numel(), "pages")
     _want(refs, "refs", (P,), torch.int32, dev)
     if src is not None:
-        n = src.numel()
         _want(src, "src", (n,), torch.int32, dev)
     if out is None:
         out = torch.empty((n,), dtype=torch.int32, device=dev)
@@ -610,10 +617,11 @@ def gdn_pages_take(refs: torch.Tensor, n: Optional[int] = None, src: Optional[to
 def gdn_pages_ref(refs: torch.Tensor, pages: torch.Tensor, delta: int) -> None:
     """refs[p] += delta for every entry p of ``pages`` that is a page, not below 0: 1 shares
     pages, -1 frees them."""
-    dev, P, n = _device_of(refs, "refs"), refs.numel(), pages.numel()
+    delta = _int32(int(delta), "delta")
+    dev, P, n = _device_of(refs, "refs"), _int32(refs.numel(), "pages"), _int32(pages.numel(), "n")
     _want(refs, "refs", (P,), torch.int32, dev)
     _want(pages, "pages", (n,), torch.int32, dev)
-    _call(dev, "gdn_pages_ref", refs.data_ptr(), P, pages.data_ptr(), n, int(delta))
+    _call(dev, "gdn_pages_ref", refs.data_ptr(), P, pages.data_ptr(), n, delta)
 
 
 def gdn_pages_fork(refs: torch.Tensor, src: torch.Tensor, pools, page_dim: int = 0,
@@ -621,7 +629,7 @@ def gdn_pages_fork(refs: torch.Tensor, src: torch.Tensor, pools, page_dim: int =
     """A new page for each entry of ``src`` (see ``gdn_pages_take``), holding a copy of page
     src[i] in each pool of ``pools``. Returns the new pages. A refused call changes nothing."""
     desc, P = _describe_counted(refs, pools, page_dim)
-    dev, n = refs.device, src.numel()
+    dev, n = refs.device, _int32(src.numel(), "n")
     _want(refs, "refs", (P,), torch.int32, dev)
     _want(src, "src", (n,), torch.int32, dev)
     if out is None:
@@ -634,14 +642,14 @@ def gdn_pages_fork(refs: torch.Tensor, src: torch.Tensor, pools, page_dim: int =
 
 def _plan_lists(refs: torch.Tensor, table: Optional[torch.Tensor]):
     """What gdn_pages_plan writes, src | dst | map | n_live in one tensor, and the call's arguments."""
-    dev, P = _device_of(refs, "refs"), refs.numel()
+    dev, P = _device_of(refs, "refs"), _int32(refs.numel(), "pages")
     _want(refs, "refs", (P,), torch.int32, dev)
     if table is not None:
         _want(table, "table", table.shape, torch.int32, dev)
     half = P // 2
     lists = torch.empty((2 * half + P + 1,), dtype=torch.int32, device=dev)
     at = lists.data_ptr()
-    return lists, half, (refs.data_ptr(), P, _addr(table), 0 if table is None else table.numel(),
+    return lists, half, (refs.data_ptr(), P, _addr(table), 0 if table is None else _int32(table.numel(), "table entries"),
                          at, at + 4 * half, at + 8 * half, at + 8 * half + 4 * P)
 
 
@@ -699,6 +707,7 @@ def gdn_gated_norm(o: torch.Tensor, z: torch.Tensor, w: torch.Tensor, eps: float
     (tokens may be strided, not expanded), w [dv]. ``y`` may be ``o``."""
     dev, dt, shape = _device_of(o, "o"), o.dtype, o.shape
     T, Hv, dv = shape
+    _int32(Hv, "Hv")
     _want(o, "o", shape, dt, dev)
     _want_view(z, "z", shape, dt, dev)
     _want(w, "w", (dv,), dt, dev)
@@ -718,6 +727,7 @@ def gdn_gated_norm_bwd(o: torch.Tensor, z: torch.Tensor, w: torch.Tensor, dy: to
     a token-strided view."""
     dev, dt, shape = _device_of(o, "o"), o.dtype, o.shape
     T, Hv, dv = shape
+    _int32(Hv, "Hv")
     do = torch.empty_like(o) if do is None else do
     dz = torch.empty(shape, dtype=dt, device=dev) if dz is None else dz
     dw = torch.empty((dv,), dtype=torch.float32, device=dev) if dw is None else dw
@@ -742,6 +752,7 @@ def gdn_add_norm(x: torch.Tensor, residual: torch.Tensor, w: torch.Tensor, scale
     Returns (n, h)."""
     dev, dt, shape, res = _device_of(x, "x"), x.dtype, x.shape, residual.dtype
     T, D = shape
+    _int32(D, "D")
     h = torch.empty_like(residual) if h is None else h
     n = torch.empty_like(x) if n is None else n
     _want(x, "x", shape, dt, dev)
@@ -763,6 +774,7 @@ def gdn_add_norm_bwd(h: torch.Tensor, w: torch.Tensor, dn: torch.Tensor, dh: Opt
     ``dres`` may be ``dh``; dx has dn's dtype (x, w, n and dx share it)."""
     dev, dt, shape, res = _device_of(h, "h"), dn.dtype, h.shape, h.dtype
     T, D = shape
+    _int32(D, "D")
     dres = torch.empty_like(h) if dres is None else dres
     dx = torch.empty_like(dn) if dx is None else dx
     dw = torch.empty((D,), dtype=torch.float32, device=dev) if dw is None else dw

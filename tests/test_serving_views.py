@@ -7,6 +7,7 @@ import random
 import pytest
 import torch
 
+import gated_deltanet_mixer_causal_b200 as gdn
 from gated_deltanet_mixer_causal_b200 import _lib
 from gated_deltanet_mixer_causal_b200.build import build
 
@@ -180,6 +181,18 @@ def test_gates_and_lists_need_only_their_own_alignment():
     assert "overlaps" in call(at(5, 40), at(6, 40), at(4, 4))
     assert "aligned" in call(at(5, 42), at(6), at(4)) and "aligned" in call(at(5), at(6, 1), at(4))
     assert "aligned" in call(at(5), at(6), at(4, 2))
+
+
+def test_counts_that_pass_32_bits():
+    """Refused, where ctypes would pass on their lower half: 2^32 + 1 pages as one page."""
+    i = torch.zeros(4, dtype=torch.int32)
+    many = torch.empty((2 ** 32 + 1, 16), dtype=torch.uint8, device="meta")
+    for call in (lambda: gdn.gdn_pages_ref(i, i, 2 ** 32 - 1), lambda: gdn.gdn_pages_take(i, n=2 ** 32 + 1),
+                 lambda: _lib._pool_layout(many, "pool", 0), lambda: _lib._pool_layout(many[:, None], "pool", 1),
+                 lambda: _lib._int32(2 ** 31, "n"), lambda: _lib._int32(-2 ** 31 - 1, "n")):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    assert _lib._int32(2 ** 31 - 1, "n") == 2 ** 31 - 1
 
 
 def test_counts_keep_within_their_range():
