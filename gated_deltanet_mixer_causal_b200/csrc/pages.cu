@@ -244,12 +244,12 @@ pages_take_kernel(int32_t* refs, int32_t n_pages, const int32_t* src, int32_t n,
 // refs[p] += delta for each entry, never below 0
 __global__ void __launch_bounds__(kPlanThreads)
 pages_ref_kernel(int32_t* refs, int32_t n_pages, const int32_t* pages, int32_t n, int32_t delta) {
-  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+  for (int64_t i = threadIdx.x; i < n; i += kPlanThreads) {
     const int32_t p = pages[i];
     if (p >= 0 && p < n_pages) atomicAdd(&refs[p], delta);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+  for (int64_t i = threadIdx.x; i < n; i += kPlanThreads) {
     const int32_t p = pages[i];
     if (p >= 0 && p < n_pages) atomicMax(&refs[p], 0);
   }
@@ -294,7 +294,7 @@ pages_plan_kernel(int32_t* refs, int32_t n_pages, int32_t* table, int32_t n_tabl
   // a free page's count is 0, also where a caller left it below
   __syncthreads();
   for (int64_t p = live_all + threadIdx.x; p < n_pages; p += kPlanThreads) refs[p] = 0;
-  for (int i = threadIdx.x; i < n_table; i += kPlanThreads) {
+  for (int64_t i = threadIdx.x; i < n_table; i += kPlanThreads) {
     const int32_t p = table[i];
     if (p >= 0 && p < n_pages) table[i] = map[p];
   }

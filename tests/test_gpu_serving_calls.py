@@ -205,3 +205,16 @@ def test_norms_fed_by_the_launch_before(cuda_device, dt):
     slow = chain(torch.cuda.synchronize)
     assert all(torch.equal(p, q) for p, q in zip(once, slow))
     assert all(torch.isfinite(t).all() for t in once)
+
+
+def test_lists_of_nearly_2_to_the_31(cuda_device):
+    """The longest list and table that a call takes: an index that steps over the end of 32 bits."""
+    n, dev = 2 ** 31 - 512, cuda_device
+    pages = torch.full((n,), -1, dtype=torch.int32, device=dev)
+    pages[0], pages[-1] = 5, 3
+    refs = ints([0, 0, 0, 1, 0, 2], dev)
+    gdn.gdn_pages_ref(refs, pages, 1)
+    assert refs.tolist() == [0, 0, 0, 2, 0, 3]
+    gdn.gdn_pages_plan(refs, pages)
+    assert refs.tolist() == [2, 3, 0, 0, 0, 0] and pages[0].item() == 1 and pages[-1].item() == 0
+    assert int((pages == -1).sum()) == n - 2
