@@ -1,14 +1,16 @@
 """Calls of the paged decode, the page operations and the norms that their documentation allows or
 refuses at its edges: views, refusals that leave everything as it was, optional outputs, every
 dispatch. Error bounds are counted as in serving_ref.py."""
+import numpy as np
 import pytest
 import torch
 
 import gated_deltanet_mixer_causal_b200 as gdn
+import oracle
 import serving_ref as R
 from parity import check
 from test_gpu_norms import add_case, add_terms, gated_case, gated_terms, slack
-from test_gpu_paged import case, ints, run_and_check
+from test_gpu_paged import case, ints, pool_of, run_and_check
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float32
@@ -218,3 +220,186 @@ def test_lists_of_nearly_2_to_the_31(cuda_device):
     gdn.gdn_pages_plan(refs, pages)
     assert refs.tolist() == [2, 3, 0, 0, 0, 0] and pages[0].item() == 1 and pages[-1].item() == 0
     assert int((pages == -1).sum()) == n - 2
+
+
+@pytest.mark.parametrize("page,n,L", [(16, 1, 1), (16, 2048, 2), (528, 700, 1), (528, 1100, 3), (16384, 31, 1), (16384, 32, 2),
+                                      (16400, 40, 1), (40960, 200, 2), (1 << 20, 33, 1), (8208, 65, 1)])
+def test_plain_copies(cuda_device, page, n, L):
+    """Every shape of a plain copy's tiles: parts of a page, a whole one, several; groups of entries
+    below and above the number from which a CTA takes four (32). Entries that are void, and that stay."""
+    P, gen = 2 * n + 3, torch.Generator().manual_seed(n)
+    order = torch.randperm(P, generator=gen).tolist()
+    src, dst = order[:n], order[n:2 * n]
+    for i in range(0, n, 7):
+        src[i] = (-1, P, dst[i])[i // 7 % 3]                            # void, void, stays
+    for i in range(3, n, 11):
+        dst[i] = -5
+    pools = [pool_of(cuda_device, (L, P, page // 4), FP, 1), pool_of(cuda_device, (L, P, 24), BF, 2)]
+    want = [p.clone() for p in pools]                                   # no order matters: copy on the device
+    pairs = [(s, d) for s, d in zip(src, dst) if 0 <= s < P and 0 <= d < P]
+    if pairs:
+        s, d = (torch.tensor(v, device=cuda_device) for v in zip(*pairs))
+        for w, p in zip(want, pools):
+            w[:, d] = p[:, s]
+    gdn.gdn_pages_copy(pools, ints(src, cuda_device), ints(dst, cuda_device), page_dim=1, plain=True)
+    assert all(torch.equal(p, w) for p, w in zip(pools, want))
+
+
+@pytest.mark.parametrize("P,page", [(200, 20000), (5000, 16400), (300, 528)])
+def test_compactions_of_larger_pages(cuda_device, P, page):
+    gen = torch.Generator().manual_seed(P)
+    refs = torch.randint(0, 3, (P,), generator=gen).tolist()
+    pool = pool_of(cuda_device, (P, page // 4), FP, 3)
+    new, _, m, n_live, back, holes = R.planned(refs, [])
+    want = R.copied(pool, pool, back, holes, 0)
+    t = ints(refs, cuda_device)
+    got_map, live = gdn.gdn_pages_compact(t, None, pool)
+    assert t.tolist() == new and got_map.tolist() == m and live.tolist() == [n_live] and torch.equal(pool.cpu(), want)
+
+
+@pytest.mark.parametrize("act,st,d,n,gate", [(BF, FP, 128, 1, False), (FP, FP, 64, 3, False), (BF, BF, 32, 2, False),
+                                             (FP, BF, 128, 2, False), (BF, FP, 128, 2, True)])
+def test_paged_scale(cuda_device, act, st, d, n, gate):
+    c = case(cuda_device, 4, n, 2, 4, d, act, st, 6, seed=13, gate=gate)
+    run_and_check(f"paged scale {act} {d} {n}", c, [5, 0, 3, -1], None, None, cuda_device, eps=1e-3, scale=0.0884)
+
+
+def sizes_against_outputs(c, read, n_valid):
+    """(alpha |S before| + |u|) / |o before its norm| for every valid token and head, [B, n, Hv], else 1.
+
+    o = alpha S q + u (k.q) is a sum of products of a unit vector with S and of u, so its fp32 error is
+    in proportion to |S| and |u| and not to what is left of them in o. A sequence that begins here has
+    o = u (k.q): with k.q = 1e-4 it carries 1e4 times the error of k.q, which the output norm then
+    takes over where eps binds. |u| = |S after - alpha S before|, since |k| = 1."""
+    B, n, _ = c["x"].shape
+    P, Hv, d, _ = c["state"].shape
+    ratio = torch.ones(B, n, Hv, dtype=torch.float64)
+    for b in range(B):
+        fresh = not 0 <= read[b] < P
+        S = np.zeros((1, Hv, d, d)) if fresh else R.f64(c["state"][read[b]])[None].numpy()
+        taps = np.zeros((1, 3, c["x"].shape[2])) if fresh else R.f64(c["conv"][read[b]])[None].numpy()
+        for t in range(min(max(n_valid[b], 0), n)):
+            old = np.exp(R.f64(c["g"][b, t]).numpy())[:, None, None] * S[0]
+            o, S, taps = oracle.decode_step(R.f64(c["x"][b, t])[None].numpy(), R.f64(c["conv_w"]).numpy(), taps,
+                                            R.f64(c["g"][b, t])[None].numpy(), R.f64(c["beta"][b, t])[None].numpy(), S,
+                                            c["Hk"], Hv, d, d, 1.0)
+            size = np.linalg.norm(old, axis=(1, 2)) + np.linalg.norm(S[0] - old, axis=(1, 2))
+            ratio[b, t] = torch.from_numpy(np.maximum(size / np.maximum(np.linalg.norm(o[0], axis=1), 1e-30), 1.0))
+    return ratio
+
+
+@pytest.mark.parametrize("B,Hk,Hv,d,n,act,st", [
+    (150, 16, 32, 64, 2, BF, FP), (150, 16, 32, 64, 2, BF, BF), (150, 16, 32, 64, 2, FP, FP), (150, 16, 32, 64, 2, FP, BF),
+    (160, 16, 48, 32, 3, BF, BF), (160, 16, 48, 32, 3, FP, FP), (300, 16, 16, 16, 3, BF, FP), (300, 16, 16, 16, 3, FP, BF),
+    (80, 16, 16, 64, 1, BF, BF)])
+def test_paged_many_narrow_heads_with_everything(cuda_device, act, st, B, Hk, Hv, d, n):
+    """CTAs of several key heads (heads below 128 in batches that fill the GPU): gate and norm,
+    scattered pages, sequences that begin here, a page for each token or none, ragged counts."""
+    P, gen = B * (n + 1) + 5, torch.Generator().manual_seed(B + d)
+    order = torch.randperm(P, generator=gen).tolist()
+    read = [-1 if b % 13 == 4 else order[b] for b in range(B)]
+    write = [[-1 if (b + t) % 5 == 3 else order[B + b * n + t] for t in range(n)] for b in range(B)]
+    valid = torch.randint(0, n + 2, (B,), generator=gen).tolist()
+    c = case(cuda_device, B, n, Hk, Hv, d, act, st, P, seed=B, wide=True, gate=True)
+    ratio = sizes_against_outputs(c, read, valid)
+    o = torch.full((B, n, Hv, d), 7.0, dtype=act, device=cuda_device)
+    want_o, want_s, want_c = R.paged(c["x"], c["conv_w"], c["conv"], c["state"], read, c["g"], c["beta"], Hk, write, valid,
+                                     c["z"], c["norm_w"], 1e-6, o)
+    gdn.gdn_decode_paged(c["x"], c["conv_w"], c["conv"], c["state"], ints(read, cuda_device), c["g"], c["beta"], Hk,
+                         write_pages=ints(write, cuda_device), n_valid=ints(valid, cuda_device), z=c["z"],
+                         norm_w=c["norm_w"], o=o)
+    name, fp32 = f"paged KH {act} {st} {Hk}/{Hv}x{d} n{n}", n * (3 * d + 40) * R.U
+    fast = 0.0 if act == FP else 2.0 ** -20
+    assert torch.equal(R.f64(c["conv"]), want_c)
+    off = lambda got, want, dims: (R.f64(got) - want).norm(dim=dims) / want.norm(dim=dims).clamp(min=1e-300)  # noqa: E731
+    kept = torch.tensor([p not in {q for row in write for q in row} for p in range(P)])
+    assert torch.equal(R.f64(c["state"])[kept], want_s[kept])
+    check(name, "state", off(c["state"], want_s, (2, 3)).max(), R.HALF[st] + fp32 + 4 * fast)
+    live = torch.arange(n) < torch.tensor(valid)[:, None]
+    assert (R.f64(o)[~live] == 7.0).all()
+    bound = R.HALF[act] + 2 * (fp32 + 4 * fast) * ratio
+    check(name, "o / bound", (off(o, want_o, -1) / bound)[live].max(), 1.0)
+
+
+@pytest.mark.parametrize("dt,res,D", [(BF, FP, 1024), (BF, BF, 1001), (FP, FP, 16384), (FP, BF, 40), (BF, FP, 9001)])
+def test_norm_backward_without_weight_or_input_gradient(cuda_device, dt, res, D):
+    """dw = NULL (with no workspace) and dx = NULL of the C entry points: the other gradients are the
+    same as with them."""
+    L, dev, T, stream = gdn.lib(), cuda_device, 37, torch.cuda.current_stream().cuda_stream
+    code = lambda t: 0 if t.dtype == FP else 1  # noqa: E731
+    x, r, w, dn, dh = (t.to(dev) for t in add_case(T, D, dt, res, D))
+    dx, dres, dw = gdn.gdn_add_norm_bwd(r, w, dn, dh, scale=0.5, w_add=1.0)
+    ws = torch.empty(gdn.gdn_norm_bwd_workspace_size(D), dtype=torch.uint8, device=dev)
+    for want_dx, want_dw in ((False, True), (True, False), (False, False)):
+        dx2, dres2, dw2 = torch.full_like(dx, 7), torch.full_like(dres, 7), torch.full_like(dw, 7)
+        status = L.gdn_add_norm_bwd(r.data_ptr(), w.data_ptr(), dn.data_ptr(), dh.data_ptr(), 0.5, 1.0, 1e-6, dres2.data_ptr(),
+                                    code(r), dx2.data_ptr() if want_dx else None, dw2.data_ptr() if want_dw else None,
+                                    code(dn), T, D, ws.data_ptr() if want_dw else None, ws.numel() if want_dw else 0, stream)
+        assert status == 0 and torch.equal(dres2, dres)
+        assert torch.equal(dx2, dx) if want_dx else (dx2 == 7).all()
+        assert torch.equal(dw2, dw) if want_dw else (dw2 == 7).all()
+    o, z, w, dy = (t.to(dev) for t in gated_case(T, 3, 64, dt, 9, False))
+    do, dz, _ = gdn.gdn_gated_norm_bwd(o, z, w, dy)
+    do2, dz2 = torch.empty_like(do), torch.empty_like(dz)
+    assert L.gdn_gated_norm_bwd(o.data_ptr(), z.data_ptr(), 0, w.data_ptr(), 1e-6, dy.data_ptr(), do2.data_ptr(),
+                                dz2.data_ptr(), 0, None, code(o), T, 3, 64, None, 0, stream) == 0
+    assert torch.equal(do2, do) and torch.equal(dz2, dz)
+
+
+def test_pages_captured(cuda_device):
+    """A captured fork and compaction, replayed over counts and tables that change."""
+    dev, P = cuda_device, 12
+    pool, src = pool_of(dev, (P, 40), FP, 4), ints([2, 2, 7, -1], dev)
+    refs, table = ints([0] * P, dev), ints([0, 0, 0], dev)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = gdn.gdn_pages_fork(refs, src, pool)
+        where, live = gdn.gdn_pages_compact(refs, table, pool)
+    for counts, names in (([0, 0, 3, 1, 0, 0, 0, 2, 0, 0, 0, 1], [2, 7, 11]), ([1] * 9 + [0, 0, 0], [8, 7, 2]),
+                          ([0] * P, [3, -1, 0]), ([1] * P, [0, 5, 11])):
+        refs.copy_(torch.tensor(counts)), table.copy_(torch.tensor(names))
+        new, got = R.taken(counts, src.tolist())
+        want = R.copied(pool, pool, src.tolist(), got, 0)
+        new, named, m, n_live, back, holes = R.planned(new, names)
+        want = R.copied(want, want, back, holes, 0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert out.tolist() == got and refs.tolist() == new and table.tolist() == named
+        assert where.tolist() == m and live.tolist() == [n_live] and torch.equal(pool.cpu(), want)
+
+
+def test_calls_on_two_streams_at_once(cuda_device):
+    """Decodes, forks and norms of two servers on a stream each, interleaved call by call, against the
+    same calls one server after the other."""
+    def server(seed):
+        c = case(cuda_device, 30, 1, 4, 8, 64, BF, FP, 64, seed=seed, gate=True)
+        c["refs"] = ints([1] * 30 + [0] * 34, cuda_device)
+        c["pages"] = ints(list(range(30)), cuda_device)
+        c["kept"] = []
+        return c
+
+    def step(c, i):
+        o = gdn.gdn_decode_paged(c["x"], c["conv_w"], c["conv"], c["state"], c["pages"], c["g"], c["beta"], 4, z=c["z"],
+                                 norm_w=c["norm_w"])
+        new = gdn.gdn_pages_fork(c["refs"], c["pages"], [c["state"], c["conv"]])
+        gdn.gdn_pages_ref(c["refs"], c["pages"], -1)
+        c["pages"] = new
+        do, dz, dw = gdn.gdn_gated_norm_bwd(o[:, 0], o[:, 0].contiguous() * 0.5, c["norm_w"], o[:, 0])
+        c["kept"] += [o, new, do, dz, dw]
+
+    alone = [server(1), server(2)]
+    for c in alone:
+        for i in range(12):
+            step(c, i)
+    torch.cuda.synchronize()
+    both, streams = [server(1), server(2)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for i in range(12):
+        for c, s in zip(both, streams):
+            with torch.cuda.stream(s):
+                step(c, i)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert all(torch.equal(p, q) for p, q in zip(a["kept"], b["kept"]))
+        assert torch.equal(a["state"], b["state"]) and torch.equal(a["conv"], b["conv"]) and torch.equal(a["refs"], b["refs"])
