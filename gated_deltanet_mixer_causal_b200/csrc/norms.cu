@@ -56,6 +56,13 @@ template <typename T, int VEC> struct Raw {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) u[i] = make_uint4(0, 0, 0, 0);
   }
+  // what the backward passes take for a value behind the last row: its 1 / rms is finite with any eps,
+  // so that its zero gradients add zeros to dw (zeros and eps = 0 would give 0 * inf)
+  __device__ __forceinline__ void ones() {
+    const uint32_t w = sizeof(T) == 4 ? 0x3F800000u : 0x3F803F80u;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) u[i] = make_uint4(w, w, w, w);
+  }
   // the elements [from, to) of the run one by one, zeros for the others
   __device__ __forceinline__ void load_part(const T* p, int from, int to) {
 #pragma unroll
@@ -173,7 +180,7 @@ gated_norm_bwd_kernel(const T* o, const T* z, int64_t z_stride, const T* w,
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t r = r0 + u * RPW;
-      ov[u].zero(); zv[u].zero(); dv[u].zero();
+      ov[u].ones(); zv[u].zero(); dv[u].zero();
       th[u] = div_rows(r, H, magic);
       if (r < rows) {
         ov[u].load(o + (int64_t)r * D + col);
@@ -197,8 +204,7 @@ gated_norm_bwd_kernel(const T* o, const T* z, int64_t z_stride, const T* w,
         ax = fmaf(da[i], x[i], ax);
       }
       ss = lanes_sum<LANES>(ss); ax = lanes_sum<LANES>(ax);
-      // 0 behind the last row, whose zeros would give dw inf * 0 with eps = 0
-      const float r1 = r < rows ? rsqrtf(ss * (1.0f / D) + eps) : 0.f, c = ax * r1 * r1 * (1.0f / D);
+      const float r1 = rsqrtf(ss * (1.0f / D) + eps), c = ax * r1 * r1 * (1.0f / D);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         dw[i] = fmaf(d[i], x[i] * r1, dw[i]);
@@ -415,7 +421,7 @@ add_norm_bwd_kernel(const R* h, const T* w, const T* dn, const R* dh,
   auto fetch_row = [&](int64_t r) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      hr[k].zero(); dr[k].zero();
+      hr[k].ones(); dr[k].zero();
       if (r < rows) { cols.load(hr[k], h, r, cols.at(k)); cols.load(dr[k], dn, r, cols.at(k)); }
     }
   };
@@ -452,8 +458,7 @@ add_norm_bwd_kernel(const R* h, const T* w, const T* dn, const R* dh,
       }
     }
     const float2 s = row_sum(ss, ax, sm, turn);
-    // 0 behind the last row, whose zeros would give dw inf * 0 with eps = 0
-    const float r1 = row < rows ? rsqrtf(fmaf(s.x, inv_d, eps)) : 0.f, cc = -s.y * r1 * r1 * inv_d;
+    const float r1 = rsqrtf(fmaf(s.x, inv_d, eps)), cc = -s.y * r1 * r1 * inv_d;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float wf[kRun], gv[kRun];
