@@ -22,11 +22,11 @@
 // others (bf16 states: 114 us by two CTAs of 256 threads, 77 by four of 128).
 //
 // Measured, 16 / 48 heads of 128 (16 / 32 for 192 sequences), share of 2 x state bytes and the
-// rest at the copy rate: 256 sequences, fp32 states 260 us (97 %); 192, bf16 states 77 us (85 %,
-// the last of its 5.2 waves of CTAs is nearly empty); one sequence 6.4 us, with the output norm 8.
+// rest at the copy rate: 256 sequences, fp32 states 261 us (97 %); 192, bf16 states 79 us (82 %,
+// the last of its 5.2 waves of CTAs is nearly empty); one sequence 6.7 us, with the output norm 8.4.
 // From four tokens on the row loop's fp32 instructions bind instead: per token and element two
 // multiply-adds for the sums and one or two for the update (64 sequences of 4 tokens, fp32 states
-// 78 us, 82 %; of 8 tokens 106 us, 62 %; 128 of 4 with bf16 states 105 us, 63 %). Taking the sums
+// 79 us, 81 %; of 8 tokens 106 us, 61 %; 128 of 4 with bf16 states 109 us, 61 %). Taking the sums
 // of all tokens from matrix instructions on the state as it was, with a triangular recursion
 // behind them, was right but slower (135 us for the last): its chain of shuffles and shared-memory
 // reads leaves three warps a scheduler idle for most of the time.
@@ -62,11 +62,13 @@ template <typename T> __device__ __forceinline__ float silu_for(float z);
 template <> __device__ __forceinline__ float silu_for<bf16>(float z) { return silu(z); }
 template <> __device__ __forceinline__ float silu_for<float>(float z) { return z / (1.0f + expf(-z)); }
 
-// a * b + c. With fp32 activations every operation of the state's way is rounded on its own, as the
-// definition's elementary operations are, and its sums are added in the order in which a warp adds
-// up a row: states then equal those of a form put together from elementary tensor operations, and,
-// stored in bf16, round the same way (by fused operations about 1 in 10^4 went the other way, and
-// the outputs of the next call with them by 3e-5). The path is bound by HBM all the same.
+// a * b + c. With fp32 activations every product and sum on the state's way is rounded on its own, as the
+// definition's elementary operations are, and the sums are added in one fixed order (plain_dots), so that
+// a state that is stored in bf16 rounds as that of a form of elementary operations does nearly everywhere.
+// Nothing more is promised than the bound of fp32 sums: in which order such a form adds is its own affair.
+// The price is in the row loop, whose instructions bind from four tokens on: 64 sequences of 1 / 4 / 8
+// tokens, fp32 states, 74 / 103 / 159 us, with bf16 activations and fused operations 70 / 79 / 106; 256 of
+// one token 271 and 258.
 template <typename T> __device__ __forceinline__ float mul_add(float a, float b, float c);
 template <> __device__ __forceinline__ float mul_add<bf16>(float a, float b, float c) { return fmaf(a, b, c); }
 template <> __device__ __forceinline__ float mul_add<float>(float a, float b, float c) { return __fadd_rn(__fmul_rn(a, b), c); }
@@ -425,8 +427,8 @@ decode_paged_kernel(const PagedDecode a, int C, int KH) {
       const int r0 = seg * kRows / L;
       float sk[kRows], sq[kRows];
       // fp32 activations: the state decays first, and its products with k are rounded and added up one
-      // by one, in the order of a sum over lanes of a warp (fours of neighbours at 128 columns, then
-      // halves)
+      // by one. The order depends on the width: at 128 columns fours of neighbours first, then halves of
+      // the row; below, halves of the row only.
       auto plain_dots = [&](const float* vec, float (&sums)[kRows]) {
         float tot[kRows];
 #pragma unroll

@@ -12,11 +12,13 @@
 // registers between their reduction and their use. Weight gradients are summed in fp32 in a
 // fixed order: registers of a thread over its rows, the threads of a CTA, then the CTAs.
 //
-// Measured, share of the bytes at the copy rate, bf16: gated 65,536 x 48 x 128 344 us (107 %:
-// two reads for a write), its backward 8,192 x 48 x 128 85 us (90 %; the second launch that adds
-// up dw and the fp32 instructions of two sigmoid factors an element take the rest); add norm
-// backward 16,384 x 4,096 with an fp32 residual 172 us (95 %). A decode batch of 64 tokens takes
-// 2.8 and 2.4 us, of which a launch is about 2.
+// Measured by graph replay, share of the bytes at the copy rate, bf16: gated 65,536 x 48 x 128 344 us
+// on one card and 373 on another (107 and 99 %: two reads for a write; 377 as a call), its backward
+// 8,192 x 48 x 128 87 to 90 us (88 %; the second launch that adds up dw and the fp32 instructions of two
+// sigmoid factors an element take the rest; 93 as a call); add norm backward 16,384 x 4,096 with an fp32
+// residual 173 us (95 %; 179 as a call). All in fp32: gated 16,384 x 48 173 us (106 %), backward 8,192 x
+// 48 157 (98 %), add norm 16,384 x 4,096 163 (100 %), backward 222 (92 %). A decode batch of 64 tokens
+// takes 2.7 and 2.0 us, of which a launch is most.
 #include <atomic>
 
 #include "common.cuh"
@@ -642,7 +644,9 @@ cudaError_t add_bwd_long(const AddNorm& a, cudaStream_t st) {
 // two runs by 256 threads 172 us, one run by 512 226; 8,000 x 8,192, bf16: forward by 512 threads 79
 // us, by 1,024 95; 4,000 x 16,384: backward reading the row twice 198 us, by registers that spill
 // 484. Odd rows: 5,000 x 7,001, bf16: forward 66 us and backward 77, element by element 204 and
-// 588; 20,000 x 1,001 31 and 50, element by element 45 and 80.)
+// 588; 20,000 x 1,001 31 and 50, element by element 45 and 80. Odd rows of more than 8,190 columns
+// spill in the forward pass, whose three runs a thread and prefetch do not fit 64 registers: 3,000 x
+// 12,001, bf16, 104 us and backward 139 for 44 and 55 of bytes; fp32 381 and 210 for 88 and 110.)
 template <typename T, typename R, bool ODD>
 cudaError_t add_odd(const AddNorm& a, cudaStream_t st) {
   const int runs = runs_of(a.D);

@@ -5,9 +5,10 @@
 // ints per page and run in one CTA (3 to 4 us for 256 pages).
 //
 // Measured, share of the bytes at the copy rate: 200 pages of 2 MB 129 us (100 %); 256 pages of
-// 3.2 MB compacted, plan included, 69 us (90 %); one page into 8 new ones in 4 layers, with the
-// taking of the pages, 25 us (70 %; writes alone are 17 us); 64 beams of 1.1 MB in 4 layers
-// reordered in place 83 us (84 %: short runs of every page in turn, see below).
+// 3.2 MB compacted, plan included, 70 us (89 %; 75 to 78 as a call); one page into 8 new ones in 4
+// layers, with the taking of the pages, 26 us (68 %; writes alone are 17 us; 29 to 31 as a call); 64
+// beams of 1.1 MB in 4 layers reordered in place 84 us (83 %: short runs of every page in turn, see
+// below).
 #include <atomic>
 
 #include "common.cuh"

@@ -473,7 +473,8 @@ gdn_status_t gdn_pages_compact(int32_t* refs, int32_t n_pages, int32_t* table, i
  * z            token t, head h at z + t*z_stride + h*dv (elements), dtype dt; 0 means Hv*dv, else
  *              >= Hv*dv, a multiple of 8.
  * w            [dv] dtype dt.
- * Math in fp32, one rounding to dt. dv in {16, 32, 64, 128}; T*Hv < 2^31. eps >= 0.
+ * Math in fp32, one rounding to dt. dv in {16, 32, 64, 128}; T*Hv < 2^31. eps >= 0; with eps = 0 a
+ * row of zeros has no norm, and its outputs (and dw) are NaN.
  *
  * gdn_gated_norm_bwd -- its backward pass: from dy, the gradients
  *   do [T, Hv, dv], dz (strided by dz_stride like z), dtype dt, and
@@ -499,7 +500,7 @@ gdn_status_t gdn_gated_norm_bwd(const void* o, const void* z, int64_t z_stride, 
  *
  * x, n         [T, D] dtype dt.      residual, h  [T, D] dtype res_dt; h may equal residual.
  * w            [D] dtype dt; w_add is 0, or 1 for weights kept as their distance from one.
- * Math in fp32: n comes from the sum before it is rounded to res_dt. 1 <= D <= 16384.
+ * Math in fp32: n comes from the sum before it is rounded to res_dt. 1 <= D <= 16384; eps as above.
  *
  * gdn_add_norm_bwd -- its backward pass, at the h that the forward pass stored: from dn (dtype
  * dt) and dh (dtype res_dt, the gradient that reaches h on its own way, or NULL for zero),
