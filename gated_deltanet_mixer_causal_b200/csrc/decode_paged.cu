@@ -62,10 +62,10 @@ template <typename T> __device__ __forceinline__ float silu_for(float z);
 template <> __device__ __forceinline__ float silu_for<bf16>(float z) { return silu(z); }
 template <> __device__ __forceinline__ float silu_for<float>(float z) { return z / (1.0f + expf(-z)); }
 
-// a * b + c. With fp32 activations every product and sum on the state's way is rounded on its own, as the
-// definition's elementary operations are, and the sums are added in one fixed order (plain_dots), so that
-// a state that is stored in bf16 rounds as that of a form of elementary operations does nearly everywhere.
-// Nothing more is promised than the bound of fp32 sums: in which order such a form adds is its own affair.
+// a * b + c. With fp32 activations every product and sum on the state's way is rounded on its own, in one
+// fixed order of sums (plain_dots), as in a form of elementary operations; fused operations made about
+// 1 in 10^4 of the states stored in bf16 round to the other neighbour than such a form's. Nothing more is
+// promised than the bound of fp32 sums: in which order such a form adds is its own affair.
 // The price is in the row loop, whose instructions bind from four tokens on: 64 sequences of 1 / 4 / 8
 // tokens, fp32 states, 74 / 103 / 159 us, with bf16 activations and fused operations 70 / 79 / 106; 256 of
 // one token 271 and 258.
